@@ -256,7 +256,7 @@ def _prepare_own(case, s):
         s["sv"] = B.SpecVerify(case["B"], 1, V, kind)
         state = dict(slots=s["slots"], counts=s["counts"], seen=s["seen"], n_slots=case["slots"])
         s["args"] = [B.make_history_args(case["B"], tokens=s["prompt"], token_offsets=s["prompt_off"],
-                                         max_tokens=s["most"], kind=B.SV_HISTORY_PROMPT, reset=s["reset"], **state),
+                                         n_tokens=s["prompt"].numel(), max_tokens=s["most"], kind=B.SV_HISTORY_PROMPT, reset=s["reset"], **state),
                      B.make_history_args(case["B"], tokens=s["output"], token_stride=case["output"],
                                          max_tokens=case["output"], kind=B.SV_HISTORY_OUTPUT, **state)]
         return
@@ -288,7 +288,8 @@ def _prepare_own(case, s):
                      history_seen=s["seen"], n_slots=s["counts"].shape[0], slots=s["slots"], repetition=s["rep"],
                      frequency=s["freq"], presence=s["pres"])
         if s["bias_tok"].numel():
-            rules.update(bias_offsets=s["bias_off"], bias_tokens=s["bias_tok"], bias_values=s["bias_val"])
+            rules.update(bias_offsets=s["bias_off"], bias_tokens=s["bias_tok"], bias_values=s["bias_val"],
+                         n_biases=s["bias_tok"].numel())
     packed = s["row_off"] if case.get("packed") else None
     s["args"] = B.make_process_args(Bn, rows, row0=row0, logits_in=src, in_strides=(rows * V, V), logits_out=dst,
                                     out_strides=(rows * V, V), row_offsets=packed, masks=s["masks"],

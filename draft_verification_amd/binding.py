@@ -25,10 +25,16 @@ EXPORTED = (
     "spec_verify_status_string", "spec_verify_timing_begin", "spec_verify_timing_end",
     "spec_verify_kernel_count", "spec_verify_kernel_name", "spec_verify_sched_check", "spec_verify_schedule",
     "spec_verify_conf_check", "spec_verify_confidence", "spec_verify_run_noalloc",
+    "spec_verify_process_check", "spec_verify_process", "spec_verify_history_check", "spec_verify_history",
+    "spec_verify_head_packed_bytes", "spec_verify_head_pack_check", "spec_verify_head_pack",
+    "spec_verify_head_check", "spec_verify_head",
 )
 SV_MAX_CONF_DELAY = 4
 SV_MAX_SCHED_BATCH, SV_MAX_SCHED_CANDIDATES = 4096, 65536
 SV_NOALLOC_SCRATCH_BYTES = 16777216
+SV_HISTORY_PROMPT, SV_HISTORY_OUTPUT = 0, 1
+SV_W4_FP4, SV_W4_INT4 = 0, 1
+SV_MAX_HIDDEN = 65536
 
 
 class Config(ctypes.Structure):
@@ -70,6 +76,48 @@ class ConfArgs(ctypes.Structure):
         ("temperature", ctypes.c_void_p), ("reset", ctypes.c_void_p), ("delay", ctypes.c_int32),
         ("c_default", ctypes.c_float), ("conf_now", ctypes.c_void_p), ("conf_out", ctypes.c_void_p),
         ("device_status", ctypes.c_void_p),
+    ]
+
+
+class ProcessArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("row0", ctypes.c_int32),
+        ("logits_in", ctypes.c_void_p), ("in_batch_stride", ctypes.c_int64), ("in_row_stride", ctypes.c_int64),
+        ("logits_out", ctypes.c_void_p), ("out_batch_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+        ("row_offsets", ctypes.c_void_p), ("verify_len", ctypes.c_void_p),
+        ("draft_tokens", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+        ("history_counts", ctypes.c_void_p), ("history_seen", ctypes.c_void_p), ("n_slots", ctypes.c_int32),
+        ("slots", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+        ("presence", ctypes.c_void_p), ("bias_offsets", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
+        ("bias_values", ctypes.c_void_p), ("n_biases", ctypes.c_int32), ("masks", ctypes.c_void_p),
+        ("mask_stride", ctypes.c_int64), ("n_masks", ctypes.c_int32), ("mask_index", ctypes.c_void_p),
+        ("live_tokens", ctypes.c_void_p), ("device_status", ctypes.c_void_p),
+    ]
+
+
+class HistoryArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("tokens", ctypes.c_void_p),
+        ("token_stride", ctypes.c_int64), ("token_offsets", ctypes.c_void_p), ("n_tokens", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p), ("kind", ctypes.c_int32), ("slots", ctypes.c_void_p),
+        ("reset", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("seen", ctypes.c_void_p),
+        ("n_slots", ctypes.c_int32), ("device_status", ctypes.c_void_p),
+    ]
+
+
+class HeadPackArgs(ctypes.Structure):
+    _fields_ = [
+        ("hidden", ctypes.c_int32), ("format", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("weights", ctypes.c_void_p), ("weight_stride", ctypes.c_int64), ("scales", ctypes.c_void_p),
+        ("scale_stride", ctypes.c_int64), ("packed", ctypes.c_void_p),
+    ]
+
+
+class HeadArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("hidden", ctypes.c_int32), ("format", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("packed", ctypes.c_void_p), ("hidden_states", ctypes.c_void_p), ("hidden_stride", ctypes.c_int64),
+        ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
     ]
 
 
@@ -118,6 +166,14 @@ def lib() -> ctypes.CDLL:
         L.spec_verify_confidence.argtypes = [ctypes.c_void_p, ctypes.POINTER(ConfArgs), ctypes.c_void_p]
         L.spec_verify_run_noalloc.restype = ctypes.c_int
         L.spec_verify_run_noalloc.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(Args), ctypes.c_void_p]
+        L.spec_verify_head_packed_bytes.restype = ctypes.c_int64
+        L.spec_verify_head_packed_bytes.argtypes = [ctypes.POINTER(Config)] + [ctypes.c_int32] * 3
+        for name, args in (("process", ProcessArgs), ("history", HistoryArgs), ("head_pack", HeadPackArgs),
+                           ("head", HeadArgs)):
+            check_fn, run_fn = getattr(L, f"spec_verify_{name}_check"), getattr(L, f"spec_verify_{name}")
+            check_fn.restype = run_fn.restype = ctypes.c_int
+            check_fn.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(args)]
+            run_fn.argtypes = [ctypes.c_void_p, ctypes.POINTER(args), ctypes.c_void_p]
         _lib = L
     return _lib
 
@@ -188,6 +244,74 @@ def sched_check(cfg: Config, args: SchedArgs) -> int:
     return int(lib().spec_verify_sched_check(ctypes.byref(cfg), ctypes.byref(args)))
 
 
+def make_process_args(B: int, rows: int, *, logits_in, in_strides: Sequence[int], logits_out,
+                      out_strides: Sequence[int], row0: int = 0, row_offsets=None, verify_len=None,
+                      draft_tokens=None, draft_stride: int = 0, history_counts=None, history_seen=None,
+                      n_slots: int = 0, slots=None, repetition=None, frequency=None, presence=None,
+                      bias_offsets=None, bias_tokens=None, bias_values=None, n_biases: int = 0, masks=None,
+                      mask_stride: int = 0, n_masks: int = 0, mask_index=None, live_tokens=None,
+                      device_status=None) -> ProcessArgs:
+    """Fill a ProcessArgs struct (device tensors or addresses).  Strides are (batch, row) in elements."""
+    return ProcessArgs(
+        B, rows, int(row0), _addr(logits_in), int(in_strides[0]), int(in_strides[1]), _addr(logits_out),
+        int(out_strides[0]), int(out_strides[1]), _addr(row_offsets), _addr(verify_len), _addr(draft_tokens),
+        int(draft_stride), _addr(history_counts), _addr(history_seen), int(n_slots), _addr(slots),
+        _addr(repetition), _addr(frequency), _addr(presence), _addr(bias_offsets), _addr(bias_tokens),
+        _addr(bias_values), int(n_biases), _addr(masks), int(mask_stride), int(n_masks), _addr(mask_index),
+        _addr(live_tokens), _addr(device_status))
+
+
+def process_check(cfg: Config, args: ProcessArgs) -> int:
+    """Host-only check of a process call (no device work)."""
+    return int(lib().spec_verify_process_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def make_history_args(B: int, *, tokens, max_tokens: int, kind: int, counts, seen, n_slots: int,
+                      token_stride: int = 0, token_offsets=None, n_tokens: int = 0, lengths=None, slots=None,
+                      reset=None, device_status=None) -> HistoryArgs:
+    """Fill a HistoryArgs struct (device tensors or addresses)."""
+    return HistoryArgs(B, int(max_tokens), _addr(tokens), int(token_stride), _addr(token_offsets), int(n_tokens),
+                       _addr(lengths), int(kind), _addr(slots), _addr(reset), _addr(counts), _addr(seen),
+                       int(n_slots), _addr(device_status))
+
+
+def history_check(cfg: Config, args: HistoryArgs) -> int:
+    """Host-only check of a history call (no device work)."""
+    return int(lib().spec_verify_history_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def make_head_pack_args(*, hidden: int, format: int, group: int, weights, weight_stride: int, scales,
+                        scale_stride: int, packed) -> HeadPackArgs:
+    """Fill a HeadPackArgs struct (device tensors or addresses)."""
+    return HeadPackArgs(int(hidden), int(format), int(group), _addr(weights), int(weight_stride), _addr(scales),
+                        int(scale_stride), _addr(packed))
+
+
+def head_pack_check(cfg: Config, args: HeadPackArgs) -> int:
+    """Host-only check of a packing call (no device work)."""
+    return int(lib().spec_verify_head_pack_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def make_head_args(rows: int, *, hidden: int, format: int, group: int, packed, hidden_states, hidden_stride: int,
+                   logits, logits_stride: int) -> HeadArgs:
+    """Fill a HeadArgs struct (device tensors or addresses)."""
+    return HeadArgs(int(rows), int(hidden), int(format), int(group), _addr(packed), _addr(hidden_states),
+                    int(hidden_stride), _addr(logits), int(logits_stride))
+
+
+def head_check(cfg: Config, args: HeadArgs) -> int:
+    """Host-only check of a head call (no device work)."""
+    return int(lib().spec_verify_head_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def head_packed_bytes(cfg: Config, hidden: int, format: int, group: int) -> int:
+    """Bytes of the packed weights of a head over the configuration's vocabulary."""
+    n = int(lib().spec_verify_head_packed_bytes(ctypes.byref(cfg), int(hidden), int(format), int(group)))
+    if n < 0:
+        raise SpecVerifyError(n, "spec_verify_head_packed_bytes")
+    return n
+
+
 def run_noalloc(cfg: Config, args: Args, stream: Optional[int] = None) -> None:
     """Enqueue one step without a handle: the library's static per-device
     workspace, no device allocation (see spec_verify_run_noalloc)."""
@@ -236,6 +360,34 @@ class SpecVerify:
         rc = lib().spec_verify_confidence(self._h, ctypes.byref(args), ctypes.c_void_p(stream))
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_verify_confidence")
+
+    def _enqueue(self, name: str, args, stream: Optional[int]) -> None:
+        if stream is None:
+            import torch
+            stream = torch.cuda.current_stream(self.cfg.device).cuda_stream
+        rc = getattr(lib(), name)(self._h, ctypes.byref(args), ctypes.c_void_p(stream))
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, name)
+
+    def process(self, args: ProcessArgs, stream: Optional[int] = None) -> None:
+        """Enqueue penalties, biases and grammar masks on logits on ``stream``."""
+        self._enqueue("spec_verify_process", args, stream)
+
+    def history(self, args: HistoryArgs, stream: Optional[int] = None) -> None:
+        """Enqueue an update of the token history on ``stream``."""
+        self._enqueue("spec_verify_history", args, stream)
+
+    def head_packed_bytes(self, hidden: int, format: int, group: int) -> int:
+        """Bytes that ``head_pack`` writes for this handle's vocabulary."""
+        return head_packed_bytes(self.cfg, hidden, format, group)
+
+    def head_pack(self, args: HeadPackArgs, stream: Optional[int] = None) -> None:
+        """Enqueue the packing of a 4-bit head's weights on ``stream``."""
+        self._enqueue("spec_verify_head_pack", args, stream)
+
+    def head(self, args: HeadArgs, stream: Optional[int] = None) -> None:
+        """Enqueue the 4-bit output head on ``stream``."""
+        self._enqueue("spec_verify_head", args, stream)
 
     def timing_begin(self, max_calls: int) -> None:
         rc = lib().spec_verify_timing_begin(self._h, int(max_calls))

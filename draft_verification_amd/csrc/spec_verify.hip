@@ -72,9 +72,13 @@
 
 #include <algorithm>
 #include <mutex>
-#include <tuple>
 
 #include "spec_verify.h"
+#include "sv_host.h"
+
+using sv::DeviceGuard;
+using sv::check_config;
+using sv::launch_kernel;
 
 namespace {
 
@@ -2105,25 +2109,28 @@ struct spec_verify {
     int* ev_kernel;       // [timing_max][kMaxSlots] kernel id of each timed launch, -1 unused
 };
 
-namespace {
+const spec_verify_config* sv::handle_config(const spec_verify* h) { return &h->cfg; }
 
-// Launches kernel on stream s with block threads per workgroup and returns the
-// launch's own status.  With start and stop events the events are attached to
-// the dispatch itself (hipExtLaunchKernel), so they time the kernel's
-// execution and not the queue around it.
-template <typename... KArgs, typename... Args>
-hipError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, uint32_t shmem, hipStream_t s, hipEvent_t e0,
-                         hipEvent_t e1, Args... args)
+int sv::check_config(const spec_verify_config* cfg)
 {
-    std::tuple<KArgs...> t(args...);
-    void* a[sizeof...(KArgs)];
-    std::apply([&](auto&... x) {
-        int i = 0;
-        ((a[i++] = (void*)&x), ...);
-    }, t);
-    if (e0) return hipExtLaunchKernel((const void*)kernel, grid, block, a, shmem, s, e0, e1, 0);
-    return hipLaunchKernel((const void*)kernel, grid, block, a, shmem, s);
+    if (!cfg) return SV_EINVAL;
+    if (cfg->max_batch < 1 || cfg->max_batch > SV_MAX_BATCH) return SV_EINVAL;
+    if (cfg->max_draft < 1 || cfg->max_draft > SV_MAX_DRAFT) return SV_EINVAL;
+    if (cfg->vocab < 1 || cfg->vocab > SV_MAX_VOCAB) return SV_EINVAL;
+    if (cfg->dtype != SV_F32 && cfg->dtype != SV_BF16) return SV_EUNSUPPORTED;
+    if (cfg->device < 0) return SV_EINVAL;
+    // A launch's work-item count must fit in 32 bits.  The largest launches:
+    // sv_stream over a chunk of positions (at most min(kChunkPos, K + 1), a
+    // target and a draft row each), sv_resid and sv_plan.
+    const long long ns = nsplit_of(cfg->vocab);
+    const long long gmax = std::min(kChunkPos, cfg->max_draft + 1);
+    const long long rows_wg = (long long)cfg->max_batch * 2 * gmax * ns;
+    const long long resid_wg = (long long)cfg->max_batch * ns * kParts;
+    if (std::max(rows_wg, resid_wg) * kThreads > 0xffffffffll) return SV_EUNSUPPORTED;
+    return SV_OK;
 }
+
+namespace {
 
 // Launches the kernels of a step; while per-kernel timing is on, each launch
 // carries its own start and stop events.  Keeps the first failing status.
@@ -2183,39 +2190,6 @@ bool args_vec_ok(const spec_verify_config* cfg, const spec_verify_args* a)
         if ((a->draft_batch_stride * es) % 16 || (a->draft_row_stride * es) % 16) return false;
     }
     return true;
-}
-
-struct DeviceGuard {
-    int old = -1;
-    explicit DeviceGuard(int dev)
-    {
-        if (hipGetDevice(&old) != hipSuccess) old = -1;
-        if (old != dev) (void)hipSetDevice(dev);
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (old >= 0 && hipGetDevice(&cur) == hipSuccess && cur != old) (void)hipSetDevice(old);
-    }
-};
-
-int check_config(const spec_verify_config* cfg)
-{
-    if (!cfg) return SV_EINVAL;
-    if (cfg->max_batch < 1 || cfg->max_batch > SV_MAX_BATCH) return SV_EINVAL;
-    if (cfg->max_draft < 1 || cfg->max_draft > SV_MAX_DRAFT) return SV_EINVAL;
-    if (cfg->vocab < 1 || cfg->vocab > SV_MAX_VOCAB) return SV_EINVAL;
-    if (cfg->dtype != SV_F32 && cfg->dtype != SV_BF16) return SV_EUNSUPPORTED;
-    if (cfg->device < 0) return SV_EINVAL;
-    // A launch's work-item count must fit in 32 bits.  The largest launches:
-    // sv_stream over a chunk of positions (at most min(kChunkPos, K + 1), a
-    // target and a draft row each), sv_resid and sv_plan.
-    const long long ns = nsplit_of(cfg->vocab);
-    const long long gmax = std::min(kChunkPos, cfg->max_draft + 1);
-    const long long rows_wg = (long long)cfg->max_batch * 2 * gmax * ns;
-    const long long resid_wg = (long long)cfg->max_batch * ns * kParts;
-    if (std::max(rows_wg, resid_wg) * kThreads > 0xffffffffll) return SV_EUNSUPPORTED;
-    return SV_OK;
 }
 
 // Fills the kernels' parameters of one call (after spec_verify_check).

@@ -1,0 +1,522 @@
+// Rules on logits around verification, and the token history they read
+// (spec_verify_process and spec_verify_history in include/spec_verify.h, which
+// states the formulas).
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "spec_verify.h"
+#include "sv_host.h"
+
+using sv::DeviceGuard;
+using sv::launch_kernel;
+
+namespace {
+
+constexpr int kThreads = 256; // 4 wavefronts of 64
+
+struct Rules {
+    int B, rows, row0, V, words;
+    const void* in;
+    long long ibs, irs;
+    void* out;
+    long long obs, ors;
+    const long long* roff;
+    const int* vlen;
+    const int* draft;
+    long long dstride;
+    const int* counts;
+    const unsigned* seen;
+    int n_slots;
+    const int* slots;
+    const float* rep;
+    const float* freq;
+    const float* pres;
+    const int* boff;
+    const int* btok;
+    const float* bval;
+    int n_biases;
+    const unsigned* masks;
+    long long mstride;
+    int n_masks;
+    const int* midx;
+    int* live;
+    int* status;
+    int nblk; // token blocks of a row
+};
+
+__device__ __forceinline__ void bad_input(int* status)
+{
+    if (status) __hip_atomic_fetch_or(status, SV_STATUS_BAD_INPUT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// First row and number of rows that the call processes of sequence b; a
+// negative count marks a bad one.
+__device__ __forceinline__ int rows_of(const Rules& q, int b, long long& first)
+{
+    if (q.roff) {
+        first = q.roff[b];
+        const long long n = q.roff[b + 1] - first;
+        return n < 0 || n > q.rows ? -1 : (int)n;
+    }
+    first = 0;
+    if (!q.vlen) return q.rows;
+    const int L = q.vlen[b];
+    if (L < 0) return -1;
+    return L < q.row0 ? 0 : (L - q.row0 < q.rows ? L - q.row0 + 1 : q.rows);
+}
+
+// Start values of the outputs that the workgroups of the call add to: the
+// status word, and the live counts (0 for a row that has a mask, else -1).
+__global__ __launch_bounds__(kThreads) void sv_rules_start_kernel(Rules q)
+{
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (i == 0 && q.status) *q.status = 0;
+    if (!q.live || i >= (long long)q.B * q.rows) return;
+    const int b = (int)(i / q.rows), r = (int)(i % q.rows);
+    long long first;
+    q.live[i] = q.masks && r < rows_of(q, b, first) && q.midx[i] != -1 ? 0 : -1;
+}
+
+__global__ void sv_status_clear_kernel(int* status) { *status = 0; }
+
+// Logits in memory, PT of them to a lane (16 bytes).  The vector types ask for
+// the element's alignment only: rows of odd lengths start anywhere.
+template <int DT>
+struct Vec;
+
+template <>
+struct Vec<SV_BF16> {
+    typedef unsigned short elem;
+    typedef unsigned short raw __attribute__((ext_vector_type(8), aligned(2)));
+    static constexpr int PT = 8;
+    static __device__ float get(elem x) { return __uint_as_float((unsigned)x << 16); }
+    static __device__ elem put(float x) { return __builtin_bit_cast(elem, (__bf16)x); }
+    static __device__ elem none() { return 0xff80; } // -infinity
+};
+
+template <>
+struct Vec<SV_F32> {
+    typedef float elem;
+    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
+    static constexpr int PT = 4;
+    static __device__ float get(elem x) { return x; }
+    static __device__ elem put(float x) { return x; }
+    static __device__ elem none() { return -INFINITY; }
+};
+
+// A lane's PT bits of a bit row, from token v0 (a multiple of PT).
+template <int PT>
+__device__ __forceinline__ unsigned bits_at(const unsigned* row, int v0)
+{
+    const unsigned byte = ((const unsigned char*)row)[v0 >> 3];
+    return PT == 8 ? byte : (byte >> (v0 & 4)) & 15u;
+}
+
+// One workgroup per (sequence, row, block of 256 PT tokens): a lane holds PT
+// consecutive tokens, so their seen and mask bits are one byte or half a byte.
+template <int DT, bool INPLACE>
+__device__ __forceinline__ void process_block(const Rules& q, long long item)
+{
+    typedef Vec<DT> X;
+    constexpr int PT = X::PT;
+    constexpr int SPAN = 64 * PT; // tokens of a wavefront
+    const int blk = (int)(item % q.nblk);
+    const long long rb = item / q.nblk;
+    const int r = (int)(rb % q.rows), b = (int)(rb / q.rows);
+    const bool first_lane = threadIdx.x == 0 && blk == 0;
+
+    long long first;
+    const int n = rows_of(q, b, first);
+    if (r == 0 && first_lane && n < 0) bad_input(q.status);
+    if (r >= n) return;
+
+    int slot = -1;
+    if (q.counts) {
+        slot = q.slots ? q.slots[b] : b;
+        if (slot < -1 || slot >= q.n_slots) {
+            if (first_lane) bad_input(q.status);
+            slot = -1;
+        }
+    }
+    float rep = q.rep ? q.rep[b] : 1.0f, freq = q.freq ? q.freq[b] : 0.0f, pres = q.pres ? q.pres[b] : 0.0f;
+    const bool rep_ok = rep > 0.0f && rep < INFINITY, freq_ok = fabsf(freq) < INFINITY, pres_ok = fabsf(pres) < INFINITY;
+    if (first_lane && !(rep_ok && freq_ok && pres_ok)) bad_input(q.status);
+    if (!rep_ok) rep = 1.0f;
+    if (!freq_ok) freq = 0.0f;
+    if (!pres_ok) pres = 0.0f;
+
+    const int lane = threadIdx.x & 63;
+    const int w0 = (blk * (kThreads / 64) + (threadIdx.x >> 6)) * SPAN; // the wavefront's first token
+    const int v0 = w0 + lane * PT;
+    const bool inside = v0 < q.V, whole = v0 + PT <= q.V;
+
+    // history
+    unsigned seen = 0;
+    int cnt[PT];
+#pragma unroll
+    for (int k = 0; k < PT; ++k) cnt[k] = 0;
+    if (slot >= 0 && inside) {
+        seen = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
+        if (seen) {
+            const int* c = q.counts + (long long)slot * q.V + v0;
+#pragma unroll
+            for (int k = 0; k < PT; ++k)
+                if ((seen >> k & 1) && v0 + k < q.V) cnt[k] = c[k];
+        }
+    }
+    // drafted prefix: 64 ids at a time, those of the wavefront's span one by one
+    const int j = q.draft ? q.row0 + r : 0;
+    const int* draft = q.draft + b * q.dstride;
+    for (int i0 = 0; i0 < j; i0 += 64) {
+        const int x = i0 + lane < j ? draft[i0 + lane] : 0;
+        if (blk == 0 && threadIdx.x < 64 && (unsigned)x >= (unsigned)q.V) bad_input(q.status);
+        unsigned long long hit = __ballot(i0 + lane < j && (unsigned)x < (unsigned)q.V && (unsigned)(x - w0) < (unsigned)SPAN);
+        while (hit) {
+            const int y = __shfl(x, __builtin_ctzll(hit)) - v0;
+            hit &= hit - 1;
+#pragma unroll
+            for (int k = 0; k < PT; ++k)
+                if (y == k) { seen |= 1u << k; cnt[k] += 1; }
+        }
+    }
+    // biases, likewise, added in the list's order
+    float bias[PT];
+    bool biased = false;
+#pragma unroll
+    for (int k = 0; k < PT; ++k) bias[k] = 0.0f;
+    if (q.boff) {
+        int e0 = q.boff[b], e1 = q.boff[b + 1];
+        if (e0 < 0 || e1 < e0 || e1 > q.n_biases) {
+            if (first_lane) bad_input(q.status);
+            e0 = e1 = 0;
+        }
+        for (int i0 = e0; i0 < e1; i0 += 64) {
+            const int at = min(i0 + lane, e1 - 1);
+            const int x = q.btok[at];
+            if (blk == 0 && threadIdx.x < 64 && (unsigned)x >= (unsigned)q.V) bad_input(q.status);
+            unsigned long long hit = __ballot(i0 + lane < e1 && (unsigned)x < (unsigned)q.V && (unsigned)(x - w0) < (unsigned)SPAN);
+            while (hit) {
+                const int src = __builtin_ctzll(hit);
+                const int y = __shfl(x, src) - v0;
+                const float add = q.bval[i0 + src];
+                hit &= hit - 1;
+#pragma unroll
+                for (int k = 0; k < PT; ++k)
+                    if (y == k) { bias[k] += add; biased = true; }
+            }
+        }
+    }
+    // mask
+    unsigned allow = (1u << PT) - 1;
+    const int m = q.masks ? q.midx[(long long)b * q.rows + r] : -1;
+    if (m != -1) {
+        if (m < -1 || m >= q.n_masks) {
+            if (first_lane) bad_input(q.status);
+            allow = 0;
+        } else if (inside) {
+            allow = bits_at<PT>(q.masks + m * q.mstride, v0);
+        }
+    }
+
+    const long long row = q.roff ? first + r : r;
+    const typename X::elem* src = (const typename X::elem*)q.in + (q.roff ? 0 : b * q.ibs) + row * q.irs + v0;
+    typename X::elem* dst = (typename X::elem*)q.out + (q.roff ? 0 : b * q.obs) + row * q.ors + v0;
+    int live = 0;
+    const bool count = q.live && m != -1;
+    // in place, only what a rule touches is read (or has to be counted)
+    const bool touched = seen || biased || allow != (1u << PT) - 1;
+    if (inside && (!INPLACE || touched || count)) {
+        typename X::elem x[PT];
+        if (whole) {
+            const typename X::raw raw = *(const typename X::raw*)src;
+#pragma unroll
+            for (int k = 0; k < PT; ++k) x[k] = raw[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < PT; ++k) x[k] = v0 + k < q.V ? src[k] : X::none();
+        }
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            if ((seen >> k & 1) || biased) {
+                float l = X::get(x[k]);
+                if (seen >> k & 1) l = l > 0.0f ? l / rep : l * rep;
+                l -= freq * (float)cnt[k] + (cnt[k] > 0 ? pres : 0.0f);
+                x[k] = X::put(l + bias[k]);
+            }
+            if (!(allow >> k & 1)) x[k] = X::none();
+            if (v0 + k < q.V) live += X::get(x[k]) > -INFINITY;
+        }
+        if (!INPLACE || touched) {
+            if (whole) {
+                typename X::raw raw;
+#pragma unroll
+                for (int k = 0; k < PT; ++k) raw[k] = x[k];
+                *(typename X::raw*)dst = raw;
+            } else {
+#pragma unroll
+                for (int k = 0; k < PT; ++k)
+                    if (v0 + k < q.V) dst[k] = x[k];
+            }
+        }
+    }
+    if (count) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) live += __shfl_xor(live, o);
+        if (lane == 0 && live)
+            __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+template <int DT, bool INPLACE>
+__global__ __launch_bounds__(kThreads) void sv_process_kernel(Rules q)
+{
+    const long long items = (long long)q.B * q.rows * q.nblk;
+    for (long long i = blockIdx.x; i < items; i += gridDim.x) process_block<DT, INPLACE>(q, i);
+}
+
+// ---------------------------------------------------------------- history
+
+struct Hist {
+    int B, V, words, most, kind, n_slots;
+    const int* tok;
+    long long stride;
+    const long long* off;
+    long long n_tokens;
+    const int* len;
+    const int* slots;
+    const int* reset;
+    int* counts;
+    unsigned* seen;
+    int* status;
+    int per; // workgroups per sequence
+};
+
+// Slot, first token and number of tokens of sequence b; slot -1: skipped.
+__device__ __forceinline__ int hist_seq(const Hist& q, int b, long long& first, int& n, bool tell)
+{
+    const int slot = q.slots ? q.slots[b] : b;
+    long long m = q.most;
+    first = b * q.stride;
+    bool bad = slot < -1 || slot >= q.n_slots;
+    if (q.off) {
+        first = q.off[b];
+        const long long end = q.off[b + 1];
+        m = end - first;
+        bad = bad || first < 0 || end > q.n_tokens;
+    } else if (q.len) {
+        m = q.len[b];
+    }
+    bad = bad || m < 0 || m > q.most;
+    if (bad && tell) bad_input(q.status);
+    n = bad ? 0 : (int)m;
+    return bad ? -1 : slot;
+}
+
+__global__ __launch_bounds__(kThreads) void sv_history_clear_kernel(Hist q)
+{
+    const int b = blockIdx.x / q.per, part = blockIdx.x % q.per;
+    long long first;
+    int n;
+    const int slot = hist_seq(q, b, first, n, false);
+    if (slot < 0 || !q.reset[b]) return;
+    int* c = q.counts + (long long)slot * q.V;
+    unsigned* s = q.seen + (long long)slot * q.words;
+    for (int v = part * kThreads + threadIdx.x; v < q.V; v += q.per * kThreads) c[v] = 0;
+    for (int v = part * kThreads + threadIdx.x; v < q.words; v += q.per * kThreads) s[v] = 0;
+}
+
+__global__ __launch_bounds__(kThreads) void sv_history_add_kernel(Hist q)
+{
+    const int b = blockIdx.x / q.per, part = blockIdx.x % q.per;
+    long long first;
+    int n;
+    const int slot = hist_seq(q, b, first, n, part == 0 && threadIdx.x == 0);
+    if (slot < 0) return;
+    int* c = q.counts + (long long)slot * q.V;
+    unsigned* s = q.seen + (long long)slot * q.words;
+    for (int i = part * kThreads + threadIdx.x; i < n; i += q.per * kThreads) {
+        const int v = q.tok[first + i];
+        if (v == -1) continue;
+        if ((unsigned)v >= (unsigned)q.V) {
+            bad_input(q.status);
+            continue;
+        }
+        __hip_atomic_fetch_or(s + (v >> 5), 1u << (v & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (q.kind == SV_HISTORY_OUTPUT) __hip_atomic_fetch_add(c + v, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+int words_of(int V) { return (V + 31) / 32; }
+
+template <int DT, bool INPLACE>
+hipError_t launch_process(Rules q, hipStream_t s)
+{
+    const int span = kThreads * Vec<DT>::PT;
+    q.nblk = (q.V + span - 1) / span;
+    const long long wgs = std::min((long long)q.B * q.rows * q.nblk, 0xffffffffll / kThreads);
+    return launch_kernel(sv_process_kernel<DT, INPLACE>, dim3((unsigned)wgs), dim3(kThreads), 0, s, nullptr, nullptr, q);
+}
+
+} // namespace
+
+extern "C" {
+
+int spec_verify_process_check(const spec_verify_config* cfg, const spec_verify_process_args* a)
+{
+    int rc = sv::check_config(cfg);
+    if (rc != SV_OK) return rc;
+    if (!a) return SV_EINVAL;
+    if (a->B < 0 || a->B > cfg->max_batch || a->rows < 1 || a->row0 < 0) return SV_EINVAL;
+    if ((long long)a->row0 + a->rows > (long long)cfg->max_draft + 1) return SV_EINVAL;
+    if (a->B == 0) return SV_OK;
+    const int V = cfg->vocab;
+    if (!a->logits_in || !a->logits_out || a->in_row_stride < V || a->out_row_stride < V) return SV_EINVAL;
+    const bool packed = a->row_offsets != nullptr;
+    if (packed && a->verify_len) return SV_EINVAL;
+    if (!packed) {
+        if (a->in_batch_stride < 0 || a->out_batch_stride < 0) return SV_EINVAL;
+        // no two output rows overlap, whichever of the two strides is the outer one
+        const long long by_b = a->out_batch_stride, by_r = a->out_row_stride;
+        const bool b_outer = by_b >= (long long)(a->rows - 1) * by_r + V;
+        const bool r_outer = by_b >= V && by_r >= (long long)(a->B - 1) * by_b + V;
+        if (a->B > 1 && !b_outer && !r_outer) return SV_EINVAL;
+    }
+    if (a->logits_in == a->logits_out) {
+        if (a->in_row_stride != a->out_row_stride) return SV_EINVAL;
+        if (!packed && a->in_batch_stride != a->out_batch_stride) return SV_EINVAL;
+    }
+    if (a->draft_tokens && a->draft_stride < (long long)a->row0 + a->rows - 1) return SV_EINVAL;
+    if (!a->history_counts != !a->history_seen) return SV_EINVAL;
+    if (a->history_counts && (a->n_slots < 1 || (!a->slots && a->n_slots < a->B))) return SV_EINVAL;
+    if (a->bias_offsets && (a->n_biases < 0 || (a->n_biases && (!a->bias_tokens || !a->bias_values)))) return SV_EINVAL;
+    if (a->masks && (!a->mask_index || a->n_masks < 1 || a->mask_stride < words_of(V))) return SV_EINVAL;
+    return SV_OK;
+}
+
+int spec_verify_process(spec_verify_t* h, const spec_verify_process_args* a, void* hip_stream)
+{
+    if (!h) return SV_EINVAL;
+    const spec_verify_config* cfg = sv::handle_config(h);
+    int rc = spec_verify_process_check(cfg, a);
+    if (rc != SV_OK) return rc;
+    if (a->B == 0) return SV_OK;
+    DeviceGuard guard(cfg->device);
+    hipStream_t s = (hipStream_t)hip_stream;
+    Rules q;
+    q.B = a->B;
+    q.rows = a->rows;
+    q.row0 = a->row0;
+    q.V = cfg->vocab;
+    q.words = words_of(q.V);
+    q.in = a->logits_in;
+    q.ibs = a->in_batch_stride;
+    q.irs = a->in_row_stride;
+    q.out = a->logits_out;
+    q.obs = a->out_batch_stride;
+    q.ors = a->out_row_stride;
+    q.roff = (const long long*)a->row_offsets;
+    q.vlen = a->verify_len;
+    q.draft = a->draft_tokens;
+    q.dstride = a->draft_stride;
+    q.counts = a->history_counts;
+    q.seen = a->history_seen;
+    q.n_slots = a->n_slots;
+    q.slots = a->slots;
+    q.rep = a->repetition;
+    q.freq = a->frequency;
+    q.pres = a->presence;
+    q.boff = a->n_biases ? a->bias_offsets : nullptr;
+    q.btok = a->bias_tokens;
+    q.bval = a->bias_values;
+    q.n_biases = a->n_biases;
+    q.masks = a->masks;
+    q.mstride = a->mask_stride;
+    q.n_masks = a->n_masks;
+    q.midx = a->mask_index;
+    q.live = a->live_tokens;
+    q.status = a->device_status;
+    q.nblk = 0;
+    hipError_t e = hipSuccess;
+    if (q.live || q.status) {
+        const long long rows = q.live ? (long long)q.B * q.rows : 1;
+        e = launch_kernel(sv_rules_start_kernel, dim3((unsigned)((rows + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
+                          nullptr, nullptr, q);
+    }
+    if (e == hipSuccess) {
+        const bool same = q.in == q.out;
+        if (cfg->dtype == SV_BF16) e = same ? launch_process<SV_BF16, true>(q, s) : launch_process<SV_BF16, false>(q, s);
+        else e = same ? launch_process<SV_F32, true>(q, s) : launch_process<SV_F32, false>(q, s);
+    }
+    return e == hipSuccess ? SV_OK : SV_EDEVICE;
+}
+
+int spec_verify_history_check(const spec_verify_config* cfg, const spec_verify_history_args* a)
+{
+    int rc = sv::check_config(cfg);
+    if (rc != SV_OK) return rc;
+    if (!a) return SV_EINVAL;
+    if (a->B < 0 || a->B > cfg->max_batch || a->max_tokens < 0) return SV_EINVAL;
+    if (a->kind != SV_HISTORY_PROMPT && a->kind != SV_HISTORY_OUTPUT) return SV_EINVAL;
+    if (a->B == 0) return SV_OK;
+    if (!a->counts || !a->seen || a->n_slots < 1 || (!a->slots && a->n_slots < a->B)) return SV_EINVAL;
+    if (a->max_tokens && !a->tokens) return SV_EINVAL;
+    if (a->token_offsets) {
+        if (a->lengths || a->n_tokens < 0) return SV_EINVAL;
+    } else if (a->token_stride < a->max_tokens) {
+        return SV_EINVAL;
+    }
+    return SV_OK;
+}
+
+int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, void* hip_stream)
+{
+    if (!h) return SV_EINVAL;
+    const spec_verify_config* cfg = sv::handle_config(h);
+    int rc = spec_verify_history_check(cfg, a);
+    if (rc != SV_OK) return rc;
+    if (a->B == 0) return SV_OK;
+    DeviceGuard guard(cfg->device);
+    hipStream_t s = (hipStream_t)hip_stream;
+    Hist q;
+    q.B = a->B;
+    q.V = cfg->vocab;
+    q.words = words_of(q.V);
+    q.most = a->max_tokens;
+    q.kind = a->kind;
+    q.n_slots = a->n_slots;
+    q.tok = a->tokens;
+    q.stride = a->token_stride;
+    q.off = (const long long*)a->token_offsets;
+    q.n_tokens = a->n_tokens;
+    q.len = a->lengths;
+    q.slots = a->slots;
+    q.reset = a->reset;
+    q.counts = a->counts;
+    q.seen = a->seen;
+    q.status = a->device_status;
+    q.per = 1;
+    hipError_t e = hipSuccess;
+    if (q.status) e = launch_kernel(sv_status_clear_kernel, dim3(1), dim3(1), 0, s, nullptr, nullptr, q.status);
+    // workgroups per sequence: enough for the work, within 2^32 work-items in all
+    const long long cap = std::max(1ll, 0xffffffffll / kThreads / q.B);
+    auto parts = [&](long long items) {
+        return (int)std::min(cap, std::max(1ll, (items + kThreads - 1) / kThreads));
+    };
+    if (e == hipSuccess && q.reset) {
+        q.per = std::min(64, parts(q.V));
+        e = launch_kernel(sv_history_clear_kernel, dim3((unsigned)((long long)q.B * q.per)), dim3(kThreads), 0, s, nullptr,
+                          nullptr, q);
+    }
+    if (e == hipSuccess) {
+        q.per = std::min(64, parts(q.most));
+        e = launch_kernel(sv_history_add_kernel, dim3((unsigned)((long long)q.B * q.per)), dim3(kThreads), 0, s, nullptr,
+                          nullptr, q);
+    }
+    return e == hipSuccess ? SV_OK : SV_EDEVICE;
+}
+
+} // extern "C"

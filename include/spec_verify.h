@@ -336,6 +336,192 @@ int spec_verify_sched_check(const spec_verify_config* cfg, const spec_verify_sch
 /* Enqueue the admission decision on hip_stream (a hipStream_t, or NULL). */
 int spec_verify_schedule(spec_verify_t* h, const spec_verify_sched_args* a, void* hip_stream);
 
+/*
+ * The path around verification: the 4-bit output head that makes the logits
+ * (spec_verify_head), the requests' own rules on them (spec_verify_process),
+ * and the token history those rules read (spec_verify_history).  In one step:
+ *   head -> process -> (draft draw) ... head -> process -> spec_verify_run ->
+ *   history, with out_tokens as the tokens.
+ * These calls use the handle's configuration (vocabulary, logits type, device,
+ * batch limits) and none of its workspace: they may overlap with each other
+ * and with the calls above, on one handle, as long as their buffers allow it.
+ * Like the calls above they check their arguments on the host, only enqueue
+ * kernels on the given stream (so they may be captured in a HIP graph), and
+ * return SV_EINVAL / SV_EUNSUPPORTED with nothing enqueued, or SV_EDEVICE.
+ *
+ * Rules on logits: penalties for repeated tokens, biases, grammar masks.
+ *
+ * Row r of sequence b holds the logits of place j = row0 + r of its block: j
+ * drafted tokens x_1 .. x_j precede it there, after the sequence's history.
+ * For every token v of the row, with
+ *   c_v     history_counts[slot][v] (where seen) + the number of i <= j with x_i = v,
+ *   seen_v  bit v of history_seen[slot], or v is one of x_1 .. x_j:
+ *   l1  = seen_v ? (l > 0 ? l / repetition : l * repetition) : l
+ *   l2  = l1 - (frequency * c_v + presence * [c_v > 0])
+ *   l3  = l2 + the biases of v, in the order of the list
+ *   out = the row's mask allows v ? l3 : -infinity
+ * in fp32, rounded once to the logits' type.  NaN and infinite logits follow
+ * these formulas; a token that the mask excludes is -infinity whatever its
+ * logit.  A row whose mask leaves nothing is -infinity throughout, and its
+ * live_tokens is 0: such a row must not be sampled or verified.
+ *
+ * Layout.  Dense: rows 0 .. rows-1 of sequence b at logits + b*batch_stride +
+ * r*row_stride, and with verify_len only those with row0 + r <= verify_len[b].
+ * Packed (row_offsets): its rows are row_offsets[b] .. row_offsets[b+1]-1, at
+ * most `rows` of them (batch strides unused).  Any strides >= V and any
+ * alignment of the type are taken; 16-byte aligned rows are fastest.
+ * logits_out is logits_in itself with the same strides (in place), or does
+ * not overlap it.  In place, only tokens that a rule touches are read or
+ * written.  Rows that are not processed keep their contents.
+ *
+ * The history of a slot is history_counts int32 [n_slots][V], how often each
+ * token was generated, and history_seen uint32 [n_slots][ceil(V/32)], bit v%32
+ * of word v/32 set for every token of the prompt or the output.  Both start at
+ * zero (or at a reset) and are kept by spec_verify_history.  slots[b] is the
+ * slot of sequence b (-1: no history); NULL: slot b.
+ *
+ * Masks: uint32 [n_masks][mask_stride], bit v%32 of word v/32 set: v allowed;
+ * mask_index int32 [B][rows] picks each row's (-1: none; rows of a packed
+ * batch are indexed by b and r alike).
+ *
+ * Outputs: logits_out; optional live_tokens int32 [B][rows], for a processed
+ * row with a mask the number of tokens above -infinity, -1 for other rows;
+ * optional device_status int32 [1], 0 or SV_STATUS_BAD_INPUT if a device value
+ * was out of range: a row count outside [0, rows] or a negative verify length
+ * (none of the sequence's rows is processed), a slot outside [-1, n_slots) (no
+ * history), a drafted id outside [0, V) or a bias id outside [0, V) (ignored),
+ * bias_offsets outside [0, n_biases] or descending (no biases), a mask index
+ * outside [-1, n_masks) (the row is left without a token), a repetition that
+ * is not finite and positive (1) or another penalty that is not finite (0).
+ * Deterministic: sums have a fixed order and the only atomics are on integers.
+ */
+typedef struct {
+    int32_t B, rows;                /* 0 <= B <= max_batch; 1 <= rows */
+    int32_t row0;                   /* >= 0; row0 + rows <= max_draft + 1 */
+    const void* logits_in;
+    int64_t in_batch_stride, in_row_stride;
+    void* logits_out;
+    int64_t out_batch_stride, out_row_stride;
+    const int64_t* row_offsets;     /* optional device [B+1]: packed rows */
+    const int32_t* verify_len;      /* optional device [B] (dense rows only) */
+    const int32_t* draft_tokens;    /* optional device [B][draft_stride]; NULL: no drafted tokens precede */
+    int64_t draft_stride;           /* >= row0 + rows - 1 */
+    const int32_t* history_counts;  /* device [n_slots][V]; NULL (with history_seen): no history */
+    const uint32_t* history_seen;   /* device [n_slots][ceil(V/32)] */
+    int32_t n_slots;                /* >= B without slots */
+    const int32_t* slots;           /* optional device [B] */
+    const float* repetition;        /* optional device [B]; NULL: 1 */
+    const float* frequency;         /* optional device [B]; NULL: 0 */
+    const float* presence;          /* optional device [B]; NULL: 0 */
+    const int32_t* bias_offsets;    /* optional device [B+1]: biases of sequence b in the two lists */
+    const int32_t* bias_tokens;     /* device [n_biases], in any order; a token may come twice */
+    const float* bias_values;       /* device [n_biases] */
+    int32_t n_biases;
+    const uint32_t* masks;          /* optional device [n_masks][mask_stride] */
+    int64_t mask_stride;            /* >= ceil(V/32) words */
+    int32_t n_masks;
+    const int32_t* mask_index;      /* device [B][rows] */
+    int32_t* live_tokens;           /* optional device [B][rows] */
+    int32_t* device_status;         /* optional device [1] */
+} spec_verify_process_args;
+
+int spec_verify_process_check(const spec_verify_config* cfg, const spec_verify_process_args* a);
+int spec_verify_process(spec_verify_t* h, const spec_verify_process_args* a, void* hip_stream);
+
+/*
+ * Token history: adds tokens to the slots that spec_verify_process reads.
+ *
+ * Sequence b's tokens are tokens[b*token_stride ..] or, with token_offsets,
+ * tokens[token_offsets[b] .. token_offsets[b+1]-1], and of dense rows the first
+ * lengths[b] if given, else max_tokens.  An id of -1 is padding, so that
+ * out_tokens of spec_verify_run is taken as it is.  First every slot with
+ * reset[b] != 0 is cleared, then
+ *   SV_HISTORY_PROMPT marks each token as seen,
+ *   SV_HISTORY_OUTPUT marks it and adds 1 to its count.
+ * Two sequences may name one slot: it gets the tokens of both.  slots[b] = -1
+ * skips a sequence.  Counts wrap past 2^31 - 1.  device_status as above: an id outside [-1, V) (ignored),
+ * a slot outside [-1, n_slots), a length outside [0, max_tokens] or offsets
+ * outside [0, n_tokens] or descending (the sequence is skipped, its reset too).
+ */
+enum { SV_HISTORY_PROMPT = 0, SV_HISTORY_OUTPUT = 1 };
+
+typedef struct {
+    int32_t B;                      /* 0 <= B <= max_batch */
+    int32_t max_tokens;             /* >= 0: the most tokens of a sequence */
+    const int32_t* tokens;          /* device */
+    int64_t token_stride;           /* >= max_tokens (dense) */
+    const int64_t* token_offsets;   /* optional device [B+1]: flat tokens */
+    int64_t n_tokens;               /* with token_offsets: length of tokens */
+    const int32_t* lengths;         /* optional device [B] (dense) */
+    int32_t kind;                   /* SV_HISTORY_PROMPT | SV_HISTORY_OUTPUT */
+    const int32_t* slots;           /* optional device [B]; NULL: slot b */
+    const int32_t* reset;           /* optional device [B] */
+    int32_t* counts;                /* device [n_slots][V], updated */
+    uint32_t* seen;                 /* device [n_slots][ceil(V/32)], updated */
+    int32_t n_slots;                /* >= 1; >= B without slots */
+    int32_t* device_status;         /* optional device [1] */
+} spec_verify_history_args;
+
+int spec_verify_history_check(const spec_verify_config* cfg, const spec_verify_history_args* a);
+int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, void* hip_stream);
+
+/*
+ * Output head with 4-bit weights: logits[m][v] = sum_k x[m][k] W[v][k] for
+ * rows m of bf16 hidden states, summed in fp32 and rounded once to the
+ * handle's logits type.
+ *   SV_W4_FP4   W = e2m1(code) * 2^(s - 127): code 0..15 is 0, .5, 1, 1.5, 2, 3,
+ *               4, 6 and their negatives; one scale byte s per 32 values (255:
+ *               NaN).  Every product of a value and its scale has to be in
+ *               bf16's normal range or zero.
+ *   SV_W4_INT4  W = (code - 8) * s, one bf16 scale s per 32, 64 or 128 values.
+ * Source layout: weights uint8 [V][weight_stride], value k in the low (k even)
+ * or high (k odd) half of byte k/2; scales [V][scale_stride] (bytes, or bf16),
+ * group g covers k = g*group ..  hidden is a multiple of the group.
+ *
+ * The kernel reads a layout of its own: spec_verify_head_pack writes it, once
+ * when the weights are loaded, into `packed` (spec_verify_head_packed_bytes of
+ * it, 16-byte aligned, caller-owned); the source may be freed afterwards.
+ *
+ * Rows: hidden_states bf16, row m at m*hidden_stride; logits row m at
+ * m*logits_stride, so that the rows of a dense block, of packed rows, or one
+ * row of every sequence's block (logits_stride = the batch stride) are written
+ * where spec_verify_process and spec_verify_run read them.  Any strides and
+ * any alignment of the types; 16-byte aligned hidden rows are fastest.  Hidden
+ * states are finite (a row that is not gives NaN or infinities, in that row
+ * only).  A row's result does not depend on the other rows' values, and is the
+ * same from run to run.
+ */
+enum { SV_W4_FP4 = 0, SV_W4_INT4 = 1 };
+#define SV_MAX_HIDDEN 65536
+
+typedef struct {
+    int32_t hidden;                 /* 1..SV_MAX_HIDDEN, a multiple of group */
+    int32_t format;                 /* SV_W4_FP4 | SV_W4_INT4 */
+    int32_t group;                  /* FP4: 32; INT4: 32, 64 or 128 */
+    const void* weights;            /* device uint8 */
+    int64_t weight_stride;          /* bytes, >= hidden / 2 */
+    const void* scales;             /* device uint8 (FP4) or bf16 (INT4) */
+    int64_t scale_stride;           /* elements, >= hidden / group */
+    void* packed;                   /* device, 16-byte aligned */
+} spec_verify_head_pack_args;
+
+typedef struct {
+    int32_t rows;                   /* 0 <= rows <= max_batch * (max_draft + 1) */
+    int32_t hidden, format, group;  /* as packed */
+    const void* packed;
+    const void* hidden_states;      /* device bf16 */
+    int64_t hidden_stride;          /* elements, >= hidden */
+    void* logits;                   /* device, the handle's type */
+    int64_t logits_stride;          /* elements, >= V */
+} spec_verify_head_args;
+
+/* Bytes of the packed weights, or a negative status. */
+int64_t spec_verify_head_packed_bytes(const spec_verify_config* cfg, int32_t hidden, int32_t format, int32_t group);
+int spec_verify_head_pack_check(const spec_verify_config* cfg, const spec_verify_head_pack_args* a);
+int spec_verify_head_pack(spec_verify_t* h, const spec_verify_head_pack_args* a, void* hip_stream);
+int spec_verify_head_check(const spec_verify_config* cfg, const spec_verify_head_args* a);
+int spec_verify_head(spec_verify_t* h, const spec_verify_head_args* a, void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

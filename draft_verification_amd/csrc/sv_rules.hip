@@ -43,7 +43,8 @@ struct Rules {
     const int* midx;
     int* live;
     int* status;
-    int nblk; // token blocks of a row
+    int nblk;          // token blocks of a row
+    int chunk, nchunk; // rows of a workgroup, chunks of a sequence
 };
 
 __device__ __forceinline__ void bad_input(int* status)
@@ -114,43 +115,79 @@ __device__ __forceinline__ unsigned bits_at(const unsigned* row, int v0)
     return PT == 8 ? byte : (byte >> (v0 & 4)) & 15u;
 }
 
-// One workgroup per (sequence, row, block of 256 PT tokens): a lane holds PT
-// consecutive tokens, so their seen and mask bits are one byte or half a byte.
+// A lane's PT logits; past the row's end they read as -infinity.
+template <int DT>
+__device__ __forceinline__ typename Vec<DT>::raw load_logits(const typename Vec<DT>::elem* p, int v0, int V)
+{
+    typedef Vec<DT> X;
+    if (v0 + X::PT <= V) return __builtin_nontemporal_load((const typename X::raw*)p);
+    typename X::raw x;
+#pragma unroll
+    for (int k = 0; k < X::PT; ++k) x[k] = v0 + k < V ? p[k] : X::none();
+    return x;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_logits(typename Vec<DT>::elem* p, typename Vec<DT>::raw x, int v0, int V)
+{
+    typedef Vec<DT> X;
+    if (v0 + X::PT <= V) {
+        *(typename X::raw*)p = x;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < X::PT; ++k)
+        if (v0 + k < V) p[k] = x[k];
+}
+
+// One workgroup per (sequence, chunk of its rows, block of 256 PT tokens).  A
+// lane holds PT consecutive tokens, so their seen and mask bits are one byte or
+// half a byte, and keeps what the rules say of them in registers from row to
+// row: the next row adds one drafted token to it.  The rows are a plain copy
+// otherwise, bound by HBM; kAhead rows are loaded before the first is used.
+constexpr int kAhead = 4;
+
 template <int DT, bool INPLACE>
 __device__ __forceinline__ void process_block(const Rules& q, long long item)
 {
     typedef Vec<DT> X;
+    typedef typename X::elem elem;
+    typedef typename X::raw raw;
     constexpr int PT = X::PT;
     constexpr int SPAN = 64 * PT; // tokens of a wavefront
+    constexpr unsigned ALL = (1u << PT) - 1;
     const int blk = (int)(item % q.nblk);
-    const long long rb = item / q.nblk;
-    const int r = (int)(rb % q.rows), b = (int)(rb / q.rows);
-    const bool first_lane = threadIdx.x == 0 && blk == 0;
+    const long long rest = item / q.nblk;
+    const int r0 = (int)(rest % q.nchunk) * q.chunk, b = (int)(rest / q.nchunk);
+    const bool tells = threadIdx.x == 0 && blk == 0; // reports what the sequence brings
 
     long long first;
     const int n = rows_of(q, b, first);
-    if (r == 0 && first_lane && n < 0) bad_input(q.status);
-    if (r >= n) return;
+    if (tells && r0 == 0 && n < 0) bad_input(q.status);
+    if (r0 >= n) return;
+    const int r1 = min(r0 + q.chunk, n);
 
     int slot = -1;
     if (q.counts) {
         slot = q.slots ? q.slots[b] : b;
         if (slot < -1 || slot >= q.n_slots) {
-            if (first_lane) bad_input(q.status);
+            if (tells) bad_input(q.status);
             slot = -1;
         }
     }
     float rep = q.rep ? q.rep[b] : 1.0f, freq = q.freq ? q.freq[b] : 0.0f, pres = q.pres ? q.pres[b] : 0.0f;
     const bool rep_ok = rep > 0.0f && rep < INFINITY, freq_ok = fabsf(freq) < INFINITY, pres_ok = fabsf(pres) < INFINITY;
-    if (first_lane && !(rep_ok && freq_ok && pres_ok)) bad_input(q.status);
+    if (tells && !(rep_ok && freq_ok && pres_ok)) bad_input(q.status);
     if (!rep_ok) rep = 1.0f;
     if (!freq_ok) freq = 0.0f;
     if (!pres_ok) pres = 0.0f;
+    const float inv = 1.0f / rep;
 
     const int lane = threadIdx.x & 63;
     const int w0 = (blk * (kThreads / 64) + (threadIdx.x >> 6)) * SPAN; // the wavefront's first token
     const int v0 = w0 + lane * PT;
-    const bool inside = v0 < q.V, whole = v0 + PT <= q.V;
+    if (w0 >= q.V) return;
+    const bool inside = v0 < q.V;
 
     // history
     unsigned seen = 0;
@@ -159,26 +196,36 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item)
     for (int k = 0; k < PT; ++k) cnt[k] = 0;
     if (slot >= 0 && inside) {
         seen = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
+        if (v0 + PT > q.V) seen &= (1u << (q.V - v0)) - 1;
         if (seen) {
             const int* c = q.counts + (long long)slot * q.V + v0;
 #pragma unroll
             for (int k = 0; k < PT; ++k)
-                if ((seen >> k & 1) && v0 + k < q.V) cnt[k] = c[k];
+                if (seen >> k & 1) cnt[k] = c[k];
         }
     }
-    // drafted prefix: 64 ids at a time, those of the wavefront's span one by one
-    const int j = q.draft ? q.row0 + r : 0;
+    // drafted tokens, 64 ids at a time, those of the wavefront's span one by
+    // one: the first j0 precede the chunk's first row, the others a later one
+    const int j0 = q.draft ? q.row0 + r0 : 0, j1 = q.draft ? q.row0 + r1 - 1 : 0;
     const int* draft = q.draft + b * q.dstride;
-    for (int i0 = 0; i0 < j; i0 += 64) {
-        const int x = i0 + lane < j ? draft[i0 + lane] : 0;
-        if (blk == 0 && threadIdx.x < 64 && (unsigned)x >= (unsigned)q.V) bad_input(q.status);
-        unsigned long long hit = __ballot(i0 + lane < j && (unsigned)x < (unsigned)q.V && (unsigned)(x - w0) < (unsigned)SPAN);
+    unsigned later = 0;
+    for (int i0 = 0; i0 < j1; i0 += 64) {
+        const int i = i0 + lane;
+        const int x = i < j1 ? draft[i] : 0;
+        const bool fine = (unsigned)x < (unsigned)q.V;
+        if (blk == 0 && threadIdx.x < 64 && !fine) bad_input(q.status);
+        unsigned long long hit = __ballot(i < j1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
         while (hit) {
-            const int y = __shfl(x, __builtin_ctzll(hit)) - v0;
+            const int src = __builtin_ctzll(hit);
             hit &= hit - 1;
+            const int y = __shfl(x, src) - v0;
+            const bool now = i0 + src < j0;
 #pragma unroll
             for (int k = 0; k < PT; ++k)
-                if (y == k) { seen |= 1u << k; cnt[k] += 1; }
+                if (y == k) {
+                    if (now) { seen |= 1u << k; cnt[k] += 1; }
+                    else later |= 1u << k;
+                }
         }
     }
     // biases, likewise, added in the list's order
@@ -189,90 +236,101 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item)
     if (q.boff) {
         int e0 = q.boff[b], e1 = q.boff[b + 1];
         if (e0 < 0 || e1 < e0 || e1 > q.n_biases) {
-            if (first_lane) bad_input(q.status);
+            if (tells) bad_input(q.status);
             e0 = e1 = 0;
         }
         for (int i0 = e0; i0 < e1; i0 += 64) {
-            const int at = min(i0 + lane, e1 - 1);
-            const int x = q.btok[at];
+            const int x = q.btok[min(i0 + lane, e1 - 1)];
             if (blk == 0 && threadIdx.x < 64 && (unsigned)x >= (unsigned)q.V) bad_input(q.status);
             unsigned long long hit = __ballot(i0 + lane < e1 && (unsigned)x < (unsigned)q.V && (unsigned)(x - w0) < (unsigned)SPAN);
             while (hit) {
                 const int src = __builtin_ctzll(hit);
+                hit &= hit - 1;
                 const int y = __shfl(x, src) - v0;
                 const float add = q.bval[i0 + src];
-                hit &= hit - 1;
 #pragma unroll
                 for (int k = 0; k < PT; ++k)
                     if (y == k) { bias[k] += add; biased = true; }
             }
         }
     }
-    // mask
-    unsigned allow = (1u << PT) - 1;
-    const int m = q.masks ? q.midx[(long long)b * q.rows + r] : -1;
-    if (m != -1) {
-        if (m < -1 || m >= q.n_masks) {
-            if (first_lane) bad_input(q.status);
-            allow = 0;
-        } else if (inside) {
-            allow = bits_at<PT>(q.masks + m * q.mstride, v0);
-        }
-    }
+    const bool may = seen || later || biased; // some row of the chunk changes this lane's logits
 
-    const long long row = q.roff ? first + r : r;
-    const typename X::elem* src = (const typename X::elem*)q.in + (q.roff ? 0 : b * q.ibs) + row * q.irs + v0;
-    typename X::elem* dst = (typename X::elem*)q.out + (q.roff ? 0 : b * q.obs) + row * q.ors + v0;
-    int live = 0;
-    const bool count = q.live && m != -1;
-    // in place, only what a rule touches is read (or has to be counted)
-    const bool touched = seen || biased || allow != (1u << PT) - 1;
-    if (inside && (!INPLACE || touched || count)) {
-        typename X::elem x[PT];
-        if (whole) {
-            const typename X::raw raw = *(const typename X::raw*)src;
+    const long long row0 = q.roff ? first : 0;
+    const elem* src = (const elem*)q.in + (q.roff ? 0 : b * q.ibs) + v0;
+    elem* dst = (elem*)q.out + (q.roff ? 0 : b * q.obs) + v0;
+    for (int ra = r0; ra < r1; ra += kAhead) {
+        raw x[kAhead];
+        unsigned allow[kAhead];
+        bool count[kAhead], need[kAhead];
 #pragma unroll
-            for (int k = 0; k < PT; ++k) x[k] = raw[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < PT; ++k) x[k] = v0 + k < q.V ? src[k] : X::none();
-        }
-#pragma unroll
-        for (int k = 0; k < PT; ++k) {
-            if ((seen >> k & 1) || biased) {
-                float l = X::get(x[k]);
-                if (seen >> k & 1) l = l > 0.0f ? l / rep : l * rep;
-                l -= freq * (float)cnt[k] + (cnt[k] > 0 ? pres : 0.0f);
-                x[k] = X::put(l + bias[k]);
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = ra + u;
+            allow[u] = ALL;
+            count[u] = need[u] = false;
+            if (r >= r1) continue;
+            const int m = q.masks ? q.midx[(long long)b * q.rows + r] : -1;
+            if (m != -1) {
+                if (m < -1 || m >= q.n_masks) {
+                    if (tells) bad_input(q.status);
+                    allow[u] = 0;
+                } else if (inside) {
+                    allow[u] = bits_at<PT>(q.masks + m * q.mstride, v0);
+                }
+                count[u] = q.live != nullptr;
             }
-            if (!(allow >> k & 1)) x[k] = X::none();
-            if (v0 + k < q.V) live += X::get(x[k]) > -INFINITY;
+            // in place, only what a rule touches is read (or has to be counted)
+            need[u] = inside && (!INPLACE || may || allow[u] != ALL || count[u]);
+            if (need[u]) x[u] = load_logits<DT>(src + (row0 + r) * q.irs, v0, q.V);
         }
-        if (!INPLACE || touched) {
-            if (whole) {
-                typename X::raw raw;
 #pragma unroll
-                for (int k = 0; k < PT; ++k) raw[k] = x[k];
-                *(typename X::raw*)dst = raw;
-            } else {
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = ra + u;
+            if (r >= r1) break;
+            if (__any(may)) {
+                if (q.draft && r > r0) { // the drafted token between the last row and this one
+                    const int y = draft[q.row0 + r - 1] - v0;
 #pragma unroll
-                for (int k = 0; k < PT; ++k)
-                    if (v0 + k < q.V) dst[k] = x[k];
+                    for (int k = 0; k < PT; ++k)
+                        if (y == k && (later >> k & 1)) { seen |= 1u << k; cnt[k] += 1; }
+                }
+#pragma unroll
+                for (int k = 0; k < PT; ++k) {
+                    float l = X::get(x[u][k]);
+                    // l / rep: the product with 1 / rep, corrected by its remainder
+                    const float d = l * inv;
+                    const float e = fmaf(fmaf(-d, rep, l), inv, d);
+                    const float pen = l > 0.0f ? (d < INFINITY ? e : d) : l * rep;
+                    l = seen >> k & 1 ? pen : l;
+                    l -= fmaf(freq, (float)cnt[k], cnt[k] > 0 ? pres : 0.0f);
+                    const elem y = X::put(l + bias[k]);
+                    x[u][k] = may ? y : x[u][k];
+                }
+            }
+            int live = 0;
+            if (allow[u] != ALL || count[u]) {
+#pragma unroll
+                for (int k = 0; k < PT; ++k) {
+                    if (!(allow[u] >> k & 1)) x[u][k] = X::none();
+                    live += v0 + k < q.V && X::get(x[u][k]) > -INFINITY;
+                }
+            }
+            if (need[u] && (!INPLACE || may || allow[u] != ALL)) store_logits<DT>(dst + (row0 + r) * q.ors, x[u], v0, q.V);
+            if (count[u]) {
+                if (!inside) live = 0;
+#pragma unroll
+                for (int o = 32; o > 0; o >>= 1) live += __shfl_xor(live, o);
+                if (lane == 0 && live)
+                    __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
         }
-    }
-    if (count) {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) live += __shfl_xor(live, o);
-        if (lane == 0 && live)
-            __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
 template <int DT, bool INPLACE>
 __global__ __launch_bounds__(kThreads) void sv_process_kernel(Rules q)
 {
-    const long long items = (long long)q.B * q.rows * q.nblk;
+    const long long items = (long long)q.B * q.nchunk * q.nblk;
     for (long long i = blockIdx.x; i < items; i += gridDim.x) process_block<DT, INPLACE>(q, i);
 }
 
@@ -357,7 +415,14 @@ hipError_t launch_process(Rules q, hipStream_t s)
 {
     const int span = kThreads * Vec<DT>::PT;
     q.nblk = (q.V + span - 1) / span;
-    const long long wgs = std::min((long long)q.B * q.rows * q.nblk, 0xffffffffll / kThreads);
+    // A workgroup takes all rows of its sequence, so that the rules are read once,
+    // unless that leaves fewer workgroups than fill the chip (8 to each of 256
+    // compute units): then as many chunks of the rows as do.
+    const long long by_seq = (long long)q.B * q.nblk;
+    q.nchunk = (int)std::min((long long)q.rows, (2048 + by_seq - 1) / by_seq);
+    q.chunk = (q.rows + q.nchunk - 1) / q.nchunk;
+    q.nchunk = (q.rows + q.chunk - 1) / q.chunk;
+    const long long wgs = std::min(by_seq * q.nchunk, 0xffffffffll / kThreads);
     return launch_kernel(sv_process_kernel<DT, INPLACE>, dim3((unsigned)wgs), dim3(kThreads), 0, s, nullptr, nullptr, q);
 }
 
@@ -439,7 +504,7 @@ int spec_verify_process(spec_verify_t* h, const spec_verify_process_args* a, voi
     q.midx = a->mask_index;
     q.live = a->live_tokens;
     q.status = a->device_status;
-    q.nblk = 0;
+    q.nblk = q.chunk = q.nchunk = 0;
     hipError_t e = hipSuccess;
     if (q.live || q.status) {
         const long long rows = q.live ? (long long)q.B * q.rows : 1;

@@ -132,7 +132,7 @@ __device__ __forceinline__ void store_logits(typename Vec<DT>::elem* p, typename
 {
     typedef Vec<DT> X;
     if (v0 + X::PT <= V) {
-        *(typename X::raw*)p = x;
+        __builtin_nontemporal_store(x, (typename X::raw*)p);
         return;
     }
 #pragma unroll
@@ -140,15 +140,41 @@ __device__ __forceinline__ void store_logits(typename Vec<DT>::elem* p, typename
         if (v0 + k < V) p[k] = x[k];
 }
 
-// One workgroup per (sequence, chunk of its rows, block of 256 PT tokens).  A
-// lane holds PT consecutive tokens, so their seen and mask bits are one byte or
-// half a byte, and keeps what the rules say of them in registers from row to
-// row: the next row adds one drafted token to it.  The rows are a plain copy
-// otherwise, bound by HBM; kAhead rows are loaded before the first is used.
+// Orders a wavefront's LDS accesses among its own lanes (they execute in
+// order; this keeps the compiler to it).
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// One workgroup per (sequence, chunk of its rows, block of 256 PT tokens); each
+// of its wavefronts works alone on SPAN = 64 PT consecutive tokens, a lane on
+// PT of them, whose seen and mask bits are one byte or half a byte.
+//
+// A history marks a few percent of the vocabulary.  So a row is a plain copy,
+// bound by HBM, and the marked tokens are listed: the wavefront keeps the list
+// of its tokens that any row of the chunk touches, with their counts and
+// biases, in LDS, passes the row's 1 KB through LDS, and lane p changes the
+// p-th listed token there.  (Every lane computing its own PT tokens instead
+// costs 20 vector instructions a token, about what the chip can issue in the
+// time HBM takes: 737 us at B = 256, 17 rows, V = 129280 bf16 where this takes
+// 560.)  The next row adds one drafted token to the counts.  kAhead rows are
+// loaded before the first is used.
 constexpr int kAhead = 4;
 
+template <int DT>
+struct Listed {
+    static constexpr int SPAN = 64 * Vec<DT>::PT;
+    typename Vec<DT>::elem row[SPAN]; // the row's logits
+    int cnt[SPAN];                    // 1 + count of a seen token, 0 for one not seen (yet)
+    float bias[SPAN];
+    unsigned short at[SPAN];          // the touched tokens, ascending
+};
+
 template <int DT, bool INPLACE>
-__device__ __forceinline__ void process_block(const Rules& q, long long item)
+__device__ __forceinline__ void process_block(const Rules& q, long long item, Listed<DT>& s)
 {
     typedef Vec<DT> X;
     typedef typename X::elem elem;
@@ -159,7 +185,13 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item)
     const int blk = (int)(item % q.nblk);
     const long long rest = item / q.nblk;
     const int r0 = (int)(rest % q.nchunk) * q.chunk, b = (int)(rest / q.nchunk);
-    const bool tells = threadIdx.x == 0 && blk == 0; // reports what the sequence brings
+    const int lane = threadIdx.x & 63;
+    const int w0 = (blk * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * SPAN; // the wavefront's first token
+    const int v0 = w0 + lane * PT;
+    if (w0 >= q.V) return;
+    const bool inside = v0 < q.V;
+    const bool teller = w0 == 0;         // the wavefront that reports what the sequence brings
+    const bool tells = teller && lane == 0;
 
     long long first;
     const int n = rows_of(q, b, first);
@@ -181,58 +213,47 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item)
     if (!rep_ok) rep = 1.0f;
     if (!freq_ok) freq = 0.0f;
     if (!pres_ok) pres = 0.0f;
-    const float inv = 1.0f / rep;
-
-    const int lane = threadIdx.x & 63;
-    const int w0 = (blk * (kThreads / 64) + (threadIdx.x >> 6)) * SPAN; // the wavefront's first token
-    const int v0 = w0 + lane * PT;
-    if (w0 >= q.V) return;
-    const bool inside = v0 < q.V;
 
     // history
-    unsigned seen = 0;
-    int cnt[PT];
-#pragma unroll
-    for (int k = 0; k < PT; ++k) cnt[k] = 0;
+    unsigned mine = 0; // the lane's touched tokens
     if (slot >= 0 && inside) {
-        seen = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
-        if (v0 + PT > q.V) seen &= (1u << (q.V - v0)) - 1;
-        if (seen) {
-            const int* c = q.counts + (long long)slot * q.V + v0;
+        mine = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
+        if (v0 + PT > q.V) mine &= (1u << (q.V - v0)) - 1;
+    }
+    {
+        const int* c = q.counts + (long long)slot * q.V + v0;
 #pragma unroll
-            for (int k = 0; k < PT; ++k)
-                if (seen >> k & 1) cnt[k] = c[k];
+        for (int k = 0; k < PT; ++k) {
+            s.cnt[lane * PT + k] = mine >> k & 1 ? 1 + c[k] : 0;
+            s.bias[lane * PT + k] = 0.0f;
         }
     }
+    wave_sync();
     // drafted tokens, 64 ids at a time, those of the wavefront's span one by
     // one: the first j0 precede the chunk's first row, the others a later one
     const int j0 = q.draft ? q.row0 + r0 : 0, j1 = q.draft ? q.row0 + r1 - 1 : 0;
     const int* draft = q.draft + b * q.dstride;
-    unsigned later = 0;
+    auto add_draft = [&](int y) { // counts token w0 + y once more
+        if (lane == 0) {
+            const int c = s.cnt[y];
+            s.cnt[y] = c ? c + 1 : 2;
+        }
+    };
     for (int i0 = 0; i0 < j1; i0 += 64) {
         const int i = i0 + lane;
         const int x = i < j1 ? draft[i] : 0;
         const bool fine = (unsigned)x < (unsigned)q.V;
-        if (blk == 0 && threadIdx.x < 64 && !fine) bad_input(q.status);
+        if (teller && !fine) bad_input(q.status);
         unsigned long long hit = __ballot(i < j1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
         while (hit) {
             const int src = __builtin_ctzll(hit);
             hit &= hit - 1;
-            const int y = __shfl(x, src) - v0;
-            const bool now = i0 + src < j0;
-#pragma unroll
-            for (int k = 0; k < PT; ++k)
-                if (y == k) {
-                    if (now) { seen |= 1u << k; cnt[k] += 1; }
-                    else later |= 1u << k;
-                }
+            const int y = __builtin_amdgcn_readlane(x, src) - w0;
+            if (y / PT == lane) mine |= 1u << (y % PT);
+            if (i0 + src < j0) add_draft(y);
         }
     }
     // biases, likewise, added in the list's order
-    float bias[PT];
-    bool biased = false;
-#pragma unroll
-    for (int k = 0; k < PT; ++k) bias[k] = 0.0f;
     if (q.boff) {
         int e0 = q.boff[b], e1 = q.boff[b + 1];
         if (e0 < 0 || e1 < e0 || e1 > q.n_biases) {
@@ -241,97 +262,124 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item)
         }
         for (int i0 = e0; i0 < e1; i0 += 64) {
             const int x = q.btok[min(i0 + lane, e1 - 1)];
-            if (blk == 0 && threadIdx.x < 64 && (unsigned)x >= (unsigned)q.V) bad_input(q.status);
-            unsigned long long hit = __ballot(i0 + lane < e1 && (unsigned)x < (unsigned)q.V && (unsigned)(x - w0) < (unsigned)SPAN);
+            const bool fine = (unsigned)x < (unsigned)q.V;
+            if (teller && !fine) bad_input(q.status);
+            unsigned long long hit = __ballot(i0 + lane < e1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
             while (hit) {
                 const int src = __builtin_ctzll(hit);
                 hit &= hit - 1;
-                const int y = __shfl(x, src) - v0;
-                const float add = q.bval[i0 + src];
-#pragma unroll
-                for (int k = 0; k < PT; ++k)
-                    if (y == k) { bias[k] += add; biased = true; }
+                const int y = __builtin_amdgcn_readlane(x, src) - w0;
+                if (y / PT == lane) mine |= 1u << (y % PT);
+                if (lane == 0) s.bias[y] += q.bval[i0 + src];
             }
         }
     }
-    const bool may = seen || later || biased; // some row of the chunk changes this lane's logits
+    // the list
+    int listed = __popc(mine), before = listed;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(before, o);
+        if (lane >= o) before += up;
+    }
+    listed = __builtin_amdgcn_readlane(before, 63);
+    before -= __popc(mine);
+    for (unsigned m = mine; m; m &= m - 1) s.at[before++] = (unsigned short)(lane * PT + __builtin_ctz(m));
+    wave_sync();
+
+    const float inv = 1.0f / rep;
+    auto apply = [&](float l, int y) { // the rules for token w0 + y
+        const int c = s.cnt[y];
+        // l / rep: the product with 1 / rep, corrected by its remainder
+        const float d = l * inv;
+        const float e = fmaf(fmaf(-d, rep, l), inv, d);
+        if (c) l = l > 0.0f ? (d < INFINITY ? e : d) : l * rep;
+        l -= fmaf(freq, (float)(c - 1 + !c), c > 1 ? pres : 0.0f);
+        return l + s.bias[y];
+    };
 
     const long long row0 = q.roff ? first : 0;
-    const elem* src = (const elem*)q.in + (q.roff ? 0 : b * q.ibs) + v0;
-    elem* dst = (elem*)q.out + (q.roff ? 0 : b * q.obs) + v0;
-    for (int ra = r0; ra < r1; ra += kAhead) {
-        raw x[kAhead];
-        unsigned allow[kAhead];
-        bool count[kAhead], need[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int r = ra + u;
-            allow[u] = ALL;
-            count[u] = need[u] = false;
-            if (r >= r1) continue;
-            const int m = q.masks ? q.midx[(long long)b * q.rows + r] : -1;
-            if (m != -1) {
-                if (m < -1 || m >= q.n_masks) {
-                    if (tells) bad_input(q.status);
-                    allow[u] = 0;
-                } else if (inside) {
-                    allow[u] = bits_at<PT>(q.masks + m * q.mstride, v0);
-                }
-                count[u] = q.live != nullptr;
+    const elem* src = (const elem*)q.in + (q.roff ? 0 : b * q.ibs);
+    elem* dst = (elem*)q.out + (q.roff ? 0 : b * q.obs);
+    // the rows in flight: what of row r = r0 + u + i * kAhead is loaded ahead
+    raw x[kAhead];
+    unsigned allow[kAhead];
+    bool masked[kAhead];
+    auto fetch = [&](int r, raw& xr, unsigned& al, bool& mk) {
+        al = ALL;
+        mk = false;
+        if (r >= r1) return;
+        const int m = q.masks ? q.midx[(long long)b * q.rows + r] : -1;
+        mk = m != -1;
+        if (mk) {
+            if (m < -1 || m >= q.n_masks) {
+                if (tells) bad_input(q.status);
+                al = 0;
+            } else if (inside) {
+                al = bits_at<PT>(q.masks + m * q.mstride, v0);
             }
-            // in place, only what a rule touches is read (or has to be counted)
-            need[u] = inside && (!INPLACE || may || allow[u] != ALL || count[u]);
-            if (need[u]) x[u] = load_logits<DT>(src + (row0 + r) * q.irs, v0, q.V);
         }
+        // in place, an unmasked row's touched tokens are changed one by one,
+        // and a masked row's logits are read where they matter
+        if (inside && (!INPLACE || (mk && al && (q.live || mine || al != ALL))))
+            xr = load_logits<DT>(src + (row0 + r) * q.irs + v0, v0, q.V);
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(r0 + u, x[u], allow[u], masked[u]);
+    for (int ra = r0; ra < r1; ra += kAhead) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int r = ra + u;
             if (r >= r1) break;
-            if (__any(may)) {
-                if (q.draft && r > r0) { // the drafted token between the last row and this one
-                    const int y = draft[q.row0 + r - 1] - v0;
-#pragma unroll
-                    for (int k = 0; k < PT; ++k)
-                        if (y == k && (later >> k & 1)) { seen |= 1u << k; cnt[k] += 1; }
-                }
-#pragma unroll
-                for (int k = 0; k < PT; ++k) {
-                    float l = X::get(x[u][k]);
-                    // l / rep: the product with 1 / rep, corrected by its remainder
-                    const float d = l * inv;
-                    const float e = fmaf(fmaf(-d, rep, l), inv, d);
-                    const float pen = l > 0.0f ? (d < INFINITY ? e : d) : l * rep;
-                    l = seen >> k & 1 ? pen : l;
-                    l -= fmaf(freq, (float)cnt[k], cnt[k] > 0 ? pres : 0.0f);
-                    const elem y = X::put(l + bias[k]);
-                    x[u][k] = may ? y : x[u][k];
-                }
+            elem* out = dst + (row0 + r) * q.ors;
+            if (listed && q.draft && r > r0) { // the drafted token between the last row and this one
+                const int y = draft[q.row0 + r - 1] - w0;
+                if ((unsigned)y < (unsigned)SPAN && w0 + y < q.V) add_draft(y);
+                wave_sync();
             }
-            int live = 0;
-            if (allow[u] != ALL || count[u]) {
-#pragma unroll
-                for (int k = 0; k < PT; ++k) {
-                    if (!(allow[u] >> k & 1)) x[u][k] = X::none();
-                    live += v0 + k < q.V && X::get(x[u][k]) > -INFINITY;
+            if (INPLACE && !masked[u]) {
+                for (int p = lane; p < listed; p += 64) {
+                    const int y = s.at[p];
+                    out[w0 + y] = X::put(apply(X::get(out[w0 + y]), y));
                 }
-            }
-            if (need[u] && (!INPLACE || may || allow[u] != ALL)) store_logits<DT>(dst + (row0 + r) * q.ors, x[u], v0, q.V);
-            if (count[u]) {
-                if (!inside) live = 0;
+            } else {
+                if (listed) {
+                    *(raw*)&s.row[lane * PT] = x[u];
+                    wave_sync();
+                    for (int p = lane; p < listed; p += 64) {
+                        const int y = s.at[p];
+                        s.row[y] = X::put(apply(X::get(s.row[y]), y));
+                    }
+                    wave_sync();
+                    x[u] = *(const raw*)&s.row[lane * PT];
+                    wave_sync();
+                }
+                if (masked[u]) {
+                    int live = 0;
 #pragma unroll
-                for (int o = 32; o > 0; o >>= 1) live += __shfl_xor(live, o);
-                if (lane == 0 && live)
-                    __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    for (int k = 0; k < PT; ++k) {
+                        if (!(allow[u] >> k & 1)) x[u][k] = X::none();
+                        live += v0 + k < q.V && X::get(x[u][k]) > -INFINITY;
+                    }
+                    if (q.live) {
+#pragma unroll
+                        for (int o = 32; o > 0; o >>= 1) live += __shfl_xor(live, o);
+                        if (lane == 0 && live)
+                            __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    }
+                }
+                if (inside && (!INPLACE || mine || allow[u] != ALL)) store_logits<DT>(out + v0, x[u], v0, q.V);
             }
+            fetch(r + kAhead, x[u], allow[u], masked[u]);
         }
     }
 }
 
 template <int DT, bool INPLACE>
-__global__ __launch_bounds__(kThreads) void sv_process_kernel(Rules q)
+__global__ __launch_bounds__(kThreads, 6) void sv_process_kernel(Rules q)
 {
+    __shared__ __align__(16) Listed<DT> lists[kThreads / 64];
     const long long items = (long long)q.B * q.nchunk * q.nblk;
-    for (long long i = blockIdx.x; i < items; i += gridDim.x) process_block<DT, INPLACE>(q, i);
+    for (long long i = blockIdx.x; i < items; i += gridDim.x) process_block<DT, INPLACE>(q, i, lists[threadIdx.x >> 6]);
 }
 
 // ---------------------------------------------------------------- history

@@ -160,8 +160,8 @@ __device__ __forceinline__ void wave_sync()
 // p-th listed token there.  (Every lane computing its own PT tokens instead
 // costs 20 vector instructions a token, about what the chip can issue in the
 // time HBM takes: 737 us at B = 256, 17 rows, V = 129280 bf16 where this takes
-// 560.)  The next row adds one drafted token to the counts.  kAhead rows are
-// loaded before the first is used.
+// 521.)  The next row adds one drafted token to the counts.  kAhead rows are in
+// flight, and the first are asked for before the rules are read.
 constexpr int kAhead = 4;
 
 template <int DT>
@@ -173,8 +173,14 @@ struct Listed {
     unsigned short at[SPAN];          // the touched tokens, ascending
 };
 
+// What the wavefronts of a workgroup have left alive of its rows.
+struct Tally {
+    int live[64]; // of row r0 + i
+    int done;     // wavefronts that have added theirs
+};
+
 template <int DT, bool INPLACE>
-__device__ __forceinline__ void process_block(const Rules& q, long long item, Listed<DT>& s)
+__device__ __forceinline__ void process_block(const Rules& q, long long item, Listed<DT>& s, Tally& t)
 {
     typedef Vec<DT> X;
     typedef typename X::elem elem;
@@ -197,7 +203,38 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     const int n = rows_of(q, b, first);
     if (tells && r0 == 0 && n < 0) bad_input(q.status);
     if (r0 >= n) return;
-    const int r1 = min(r0 + q.chunk, n);
+    const int r1 = min(r0 + q.chunk, n); // at most 64 rows: a lane's share of what each row brings
+
+    const elem* src = (const elem*)q.in + (q.roff ? (first + r0) * q.irs : b * q.ibs + r0 * q.irs) + v0;
+    elem* dst = (elem*)q.out + (q.roff ? (first + r0) * q.ors : b * q.obs + r0 * q.ors) + w0;
+
+    // rows in flight: slot u holds row r0 + u, then r0 + u + kAhead, ...; its
+    // mask bits are asked for one turn of the slots earlier than its logits
+    raw x[kAhead];
+    unsigned allow[kAhead], allow_next[kAhead];
+    auto fetch = [&](int i, raw& xr) {
+        if (r0 + i < r1 && inside) xr = load_logits<DT>(src + i * q.irs, v0, q.V);
+    };
+    if (!INPLACE) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) fetch(u, x[u]);
+    }
+    const int my_mask = q.masks && r0 + lane < r1 ? q.midx[(long long)b * q.rows + r0 + lane] : -1;
+    const int my_draft = q.draft && r0 + lane + 1 < r1 ? q.draft[b * q.dstride + q.row0 + r0 + lane] : -1;
+    if (teller && (my_mask < -1 || my_mask >= q.n_masks) && q.masks) bad_input(q.status);
+    auto mask_of = [&](int i) { return __builtin_amdgcn_readlane(my_mask, i); }; // of row r0 + i, i < 64
+    auto fetch_mask = [&](int i, unsigned& al) {
+        al = ALL;
+        if (r0 + i >= r1) return;
+        const int m = mask_of(i);
+        if (m == -1) return;
+        al = 0; // of an index out of range
+        if (m >= 0 && m < q.n_masks && inside) al = bits_at<PT>(q.masks + m * q.mstride, v0);
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch_mask(u, allow[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch_mask(u + kAhead, allow_next[u]);
 
     int slot = -1;
     if (q.counts) {
@@ -232,7 +269,6 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     // drafted tokens, 64 ids at a time, those of the wavefront's span one by
     // one: the first j0 precede the chunk's first row, the others a later one
     const int j0 = q.draft ? q.row0 + r0 : 0, j1 = q.draft ? q.row0 + r1 - 1 : 0;
-    const int* draft = q.draft + b * q.dstride;
     auto add_draft = [&](int y) { // counts token w0 + y once more
         if (lane == 0) {
             const int c = s.cnt[y];
@@ -241,7 +277,7 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     };
     for (int i0 = 0; i0 < j1; i0 += 64) {
         const int i = i0 + lane;
-        const int x = i < j1 ? draft[i] : 0;
+        const int x = i < j1 ? q.draft[b * q.dstride + i] : 0;
         const bool fine = (unsigned)x < (unsigned)q.V;
         if (teller && !fine) bad_input(q.status);
         unsigned long long hit = __ballot(i < j1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
@@ -274,16 +310,15 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
             }
         }
     }
-    // the list
-    int listed = __popc(mine), before = listed;
+    // the list, in the order of the lanes
+    int listed = 0, at = 0;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int up = __shfl_up(before, o);
-        if (lane >= o) before += up;
+    for (int k = 0; k < PT; ++k) {
+        const unsigned long long has = __ballot(mine >> k & 1);
+        listed += __popcll(has);
+        at += __builtin_amdgcn_mbcnt_hi((unsigned)(has >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)has, 0));
     }
-    listed = __builtin_amdgcn_readlane(before, 63);
-    before -= __popc(mine);
-    for (unsigned m = mine; m; m &= m - 1) s.at[before++] = (unsigned short)(lane * PT + __builtin_ctz(m));
+    for (unsigned m = mine; m; m &= m - 1) s.at[at++] = (unsigned short)(lane * PT + __builtin_ctz(m));
     wave_sync();
 
     const float inv = 1.0f / rep;
@@ -296,50 +331,35 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
         l -= fmaf(freq, (float)(c - 1 + !c), c > 1 ? pres : 0.0f);
         return l + s.bias[y];
     };
-
-    const long long row0 = q.roff ? first : 0;
-    const elem* src = (const elem*)q.in + (q.roff ? 0 : b * q.ibs);
-    elem* dst = (elem*)q.out + (q.roff ? 0 : b * q.obs);
-    // the rows in flight: what of row r = r0 + u + i * kAhead is loaded ahead
-    raw x[kAhead];
-    unsigned allow[kAhead];
-    bool masked[kAhead];
-    auto fetch = [&](int r, raw& xr, unsigned& al, bool& mk) {
-        al = ALL;
-        mk = false;
-        if (r >= r1) return;
-        const int m = q.masks ? q.midx[(long long)b * q.rows + r] : -1;
-        mk = m != -1;
-        if (mk) {
-            if (m < -1 || m >= q.n_masks) {
-                if (tells) bad_input(q.status);
-                al = 0;
-            } else if (inside) {
-                al = bits_at<PT>(q.masks + m * q.mstride, v0);
-            }
-        }
-        // in place, an unmasked row's touched tokens are changed one by one,
-        // and a masked row's logits are read where they matter
-        if (inside && (!INPLACE || (mk && al && (q.live || mine || al != ALL))))
-            xr = load_logits<DT>(src + (row0 + r) * q.irs + v0, v0, q.V);
+    // in place, an unmasked row's touched tokens are changed one by one, and a
+    // masked row's logits are read where they matter
+    auto fetch_where = [&](int i, raw& xr, unsigned al) {
+        if (!INPLACE) fetch(i, xr);
+        else if (r0 + i < r1 && mask_of(i) != -1 && al && (q.live || mine || al != ALL)) fetch(i, xr);
     };
+    if (INPLACE) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) fetch(r0 + u, x[u], allow[u], masked[u]);
-    for (int ra = r0; ra < r1; ra += kAhead) {
+        for (int u = 0; u < kAhead; ++u) fetch_where(u, x[u], allow[u]);
+    }
+    int my_live = 0; // of row r0 + lane
+    for (int ia = 0; r0 + ia < r1; ia += kAhead) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int r = ra + u;
-            if (r >= r1) break;
-            elem* out = dst + (row0 + r) * q.ors;
-            if (listed && q.draft && r > r0) { // the drafted token between the last row and this one
-                const int y = draft[q.row0 + r - 1] - w0;
-                if ((unsigned)y < (unsigned)SPAN && w0 + y < q.V) add_draft(y);
-                wave_sync();
+            const int i = ia + u;
+            if (r0 + i >= r1) break;
+            const bool masked = mask_of(i) != -1;
+            elem* out = dst + i * q.ors;
+            if (listed && i > 0) { // the drafted token between the last row and this one
+                const int y = __builtin_amdgcn_readlane(my_draft, i - 1) - w0;
+                if ((unsigned)y < (unsigned)SPAN && w0 + y < q.V) {
+                    add_draft(y);
+                    wave_sync();
+                }
             }
-            if (INPLACE && !masked[u]) {
+            if (INPLACE && !masked) {
                 for (int p = lane; p < listed; p += 64) {
                     const int y = s.at[p];
-                    out[w0 + y] = X::put(apply(X::get(out[w0 + y]), y));
+                    out[y] = X::put(apply(X::get(out[y]), y));
                 }
             } else {
                 if (listed) {
@@ -353,23 +373,40 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
                     x[u] = *(const raw*)&s.row[lane * PT];
                     wave_sync();
                 }
-                if (masked[u]) {
+                if (masked) {
                     int live = 0;
 #pragma unroll
                     for (int k = 0; k < PT; ++k) {
                         if (!(allow[u] >> k & 1)) x[u][k] = X::none();
-                        live += v0 + k < q.V && X::get(x[u][k]) > -INFINITY;
+                        live += __popcll(__ballot(v0 + k < q.V && X::get(x[u][k]) > -INFINITY));
                     }
-                    if (q.live) {
-#pragma unroll
-                        for (int o = 32; o > 0; o >>= 1) live += __shfl_xor(live, o);
-                        if (lane == 0 && live)
-                            __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    }
+                    if (lane == i) my_live = live;
                 }
-                if (inside && (!INPLACE || mine || allow[u] != ALL)) store_logits<DT>(out + v0, x[u], v0, q.V);
+                if (inside && (!INPLACE || mine || allow[u] != ALL)) store_logits<DT>(out + lane * PT, x[u], v0, q.V);
             }
-            fetch(r + kAhead, x[u], allow[u], masked[u]);
+            allow[u] = allow_next[u];
+            fetch_where(i + kAhead, x[u], allow[u]);
+            fetch_mask(i + 2 * kAhead, allow_next[u]);
+        }
+    }
+    // The counts of the workgroup's wavefronts are joined in LDS and its last
+    // wavefront adds them to the output: one atomic instruction for all rows.
+    // (One for each row and wavefront: 42 us instead of 28 for 400 masked
+    // rows of 50257 tokens, most of it spent on their few cache lines.)
+    if (q.live && q.masks) {
+        if (my_live) __hip_atomic_fetch_add(&t.live[lane], my_live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        int done = 0;
+        if (lane == 0) done = __hip_atomic_fetch_add(&t.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        done = __builtin_amdgcn_readfirstlane(done);
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        const int waves = min(kThreads / 64, (q.V - blk * (kThreads / 64) * SPAN + SPAN - 1) / SPAN);
+        if (done == waves - 1) {
+            const int live = t.live[lane];
+            if (live)
+                __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r0 + lane, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            t.live[lane] = 0;
+            if (lane == 0) t.done = 0;
         }
     }
 }
@@ -378,8 +415,15 @@ template <int DT, bool INPLACE>
 __global__ __launch_bounds__(kThreads, 6) void sv_process_kernel(Rules q)
 {
     __shared__ __align__(16) Listed<DT> lists[kThreads / 64];
+    __shared__ Tally tally;
+    if (threadIdx.x < 64) tally.live[threadIdx.x] = 0;
+    if (threadIdx.x == 0) tally.done = 0;
+    __syncthreads();
     const long long items = (long long)q.B * q.nchunk * q.nblk;
-    for (long long i = blockIdx.x; i < items; i += gridDim.x) process_block<DT, INPLACE>(q, i, lists[threadIdx.x >> 6]);
+    for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+        process_block<DT, INPLACE>(q, i, lists[threadIdx.x >> 6], tally);
+        if (gridDim.x < items) __syncthreads(); // the tally is cleared before the next block's counts
+    }
 }
 
 // ---------------------------------------------------------------- history
@@ -465,10 +509,11 @@ hipError_t launch_process(Rules q, hipStream_t s)
     q.nblk = (q.V + span - 1) / span;
     // A workgroup takes all rows of its sequence, so that the rules are read once,
     // unless that leaves fewer workgroups than fill the chip (8 to each of 256
-    // compute units): then as many chunks of the rows as do.
+    // compute units): then as many chunks of the rows as do.  A chunk has at most
+    // 64 rows, one to a lane.
     const long long by_seq = (long long)q.B * q.nblk;
     q.nchunk = (int)std::min((long long)q.rows, (2048 + by_seq - 1) / by_seq);
-    q.chunk = (q.rows + q.nchunk - 1) / q.nchunk;
+    q.chunk = std::min(64, (q.rows + q.nchunk - 1) / q.nchunk);
     q.nchunk = (q.rows + q.chunk - 1) / q.chunk;
     const long long wgs = std::min(by_seq * q.nchunk, 0xffffffffll / kThreads);
     return launch_kernel(sv_process_kernel<DT, INPLACE>, dim3((unsigned)wgs), dim3(kThreads), 0, s, nullptr, nullptr, q);

@@ -143,25 +143,31 @@ __device__ __forceinline__ float fp4_scale(unsigned word, int p)
 }
 
 // INT4: code + 16, whose bf16 has the code in the top four bits of its
-// fraction: a shift, a mask and the exponent of 16 make two of them at once.
-__device__ __forceinline__ bf16x8 widen_int4(unsigned w)
-{
-    union { unsigned u[4]; bf16x8 v; } u;
-    u.u[0] = (w << 3 & 0x00780078u) | 0x41804180u;
-    u.u[1] = (w >> 1 & 0x00780078u) | 0x41804180u;
-    u.u[2] = (w >> 5 & 0x00780078u) | 0x41804180u;
-    u.u[3] = (w >> 9 & 0x00780078u) | 0x41804180u;
-    return u.v;
-}
+// fraction: a shift and one and-or make two of them.  The and-or takes no
+// literal and one scalar operand, so its constants are held in a scalar and a
+// vector register.
+struct Int4Bits {
+    unsigned mask, expo;
+    __device__ __forceinline__ Int4Bits() : mask(0x00780078u), expo(0x41804180u)
+    {
+        asm("" : "+s"(mask));
+        asm("" : "+v"(expo));
+    }
+    __device__ __forceinline__ bf16x8 widen(unsigned w) const
+    {
+        union { unsigned u[4]; bf16x8 v; } u;
+        u.u[0] = (w << 3 & mask) | expo;
+        u.u[1] = (w >> 1 & mask) | expo;
+        u.u[2] = (w >> 5 & mask) | expo;
+        u.u[3] = (w >> 9 & mask) | expo;
+        return u.v;
+    }
+};
 
-// acc += the INT4 scales of tile t's four rows (in the tile pair's 16 bytes) * d
-__device__ __forceinline__ void add_scaled(f32x4& acc, f32x4 d, u32x4 s, int t)
+__device__ __forceinline__ void add_scaled(f32x4& acc, f32x4 d, f32x4 s)
 {
-    const unsigned lo = s[t % 2 * 2], hi = s[t % 2 * 2 + 1];
-    acc[0] = fmaf(__uint_as_float(lo << 16), d[0], acc[0]);
-    acc[1] = fmaf(__uint_as_float(lo & 0xffff0000u), d[1], acc[1]);
-    acc[2] = fmaf(__uint_as_float(hi << 16), d[2], acc[2]);
-    acc[3] = fmaf(__uint_as_float(hi & 0xffff0000u), d[3], acc[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(s[i], d[i], acc[i]);
 }
 
 struct Head {
@@ -192,107 +198,13 @@ __device__ __forceinline__ void put4(__bf16* p, f32x4 v, int n)
         for (int i = 0; i < n; ++i) p[i] = (__bf16)v[i];
 }
 
-// One lane's part of a step: its weights of the four tiles, the scales, and 32
-// hidden values of one row.
-template <int FMT, int GROUPS>
-struct Part {
-    u32x4 w[4];
-    u32x4 x[4];
-    u32x4 s[FMT == SV_W4_INT4 ? 2 * GROUPS : 1];
-
-    __device__ __forceinline__ void load(const Head& q, long long block, int step, int lane, const unsigned short* x, bool row)
-    {
-        const int g = lane >> 4;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = __builtin_nontemporal_load((const u32x4*)(q.packed + block * 4096 + t * 1024 + lane * 16));
-        if constexpr (FMT == SV_W4_FP4) {
-            s[0] = __builtin_nontemporal_load((const u32x4*)(q.packed + q.y.scale_at + block * 256 + (lane & 15) * 16));
-        } else {
-            const unsigned char* sp = q.packed + q.y.scale_at + block * (GROUPS * 128) + g * 32;
-#pragma unroll
-            for (int u = 0; u < GROUPS; ++u) {
-                s[2 * u] = *(const u32x4*)(sp + u * 128);
-                s[2 * u + 1] = *(const u32x4*)(sp + u * 128 + 16);
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int k = step * kStep + 32 * p + 8 * g;
-            this->x[p] = u32x4{0, 0, 0, 0};
-            if (row && k < q.y.H) this->x[p] = *(const u32x4_any*)(x + k);
-        }
-    }
-
-    __device__ __forceinline__ void add(f32x4* acc) const
-    {
-        if constexpr (FMT == SV_W4_FP4) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_fp4(w[t][p], fp4_scale(s[0][t], p)), __builtin_bit_cast(bf16x8, x[p]), acc[t], 0, 0, 0);
-        } else {
-            constexpr int P = 4 / GROUPS; // products of a group
-            bf16x8 ones;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ones[k] = (__bf16)1.0f;
-#pragma unroll
-            for (int u = 0; u < GROUPS; ++u) {
-                f32x4 sum = {}; // of x over the group, in every row
-#pragma unroll
-                for (int p = u * P; p < u * P + P; ++p)
-                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, __builtin_bit_cast(bf16x8, x[p]), sum, 0, 0, 0);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    f32x4 d = sum * -24.0f;
-#pragma unroll
-                    for (int p = u * P; p < u * P + P; ++p)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_int4(w[t][p]), __builtin_bit_cast(bf16x8, x[p]), d, 0, 0, 0);
-                    add_scaled(acc[t], d, s[2 * u + t / 2], t);
-                }
-            }
-        }
-    }
-};
-
-// Up to 16 rows: one workgroup of WK wavefronts per strip, which take its steps
-// in turn (so that the workgroup reads WK blocks, one after the other in
-// memory, at a time), each with the next step's loads under way, and join
-// their sums in LDS.  Bound by the weights' HBM bytes.
-template <int FMT, int GROUPS, int WK, typename OUT>
-__global__ __launch_bounds__(64 * WK) void sv_head_rows_kernel(Head q)
+// Orders a wavefront's LDS accesses among its own lanes (they execute in
+// order; this keeps the compiler to it).
+__device__ __forceinline__ void wave_sync()
 {
-    __shared__ f32x4 part[WK][4][64];
-    const int lane = threadIdx.x & 63, c = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const long long strip = blockIdx.x % q.nstrip;
-    const int m = (int)(blockIdx.x / q.nstrip) * 16 + c;
-    const unsigned short* x = q.x + (long long)m * q.xs;
-    const bool row = m < q.M;
-    f32x4 acc[4] = {};
-
-    const long long first = strip * q.y.steps;
-    Part<FMT, GROUPS> a, b;
-    int step = wave;
-    if (step < q.y.steps) a.load(q, first + step, step, lane, x, row);
-    while (step < q.y.steps) {
-        if (step + WK < q.y.steps) b.load(q, first + step + WK, step + WK, lane, x, row);
-        a.add(acc);
-        step += WK;
-        if (step >= q.y.steps) break;
-        if (step + WK < q.y.steps) a.load(q, first + step + WK, step + WK, lane, x, row);
-        b.add(acc);
-        step += WK;
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) part[wave][t][lane] = acc[t];
-    __syncthreads();
-    if (wave >= 4) return;
-    f32x4 sum = part[0][wave][lane];
-#pragma unroll
-    for (int w = 1; w < WK; ++w) sum += part[w][wave][lane];
-    const long long v = strip * kStrip + 16 * (lane >> 4) + 4 * wave;
-    if (row && v < q.y.V) put4((OUT*)q.out + (long long)m * q.os + v, sum, (int)(q.y.V - v));
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
 // Workgroup barrier for LDS alone: global loads stay in flight across it.
@@ -303,26 +215,132 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// The sum of 8 bf16 values.
-__device__ __forceinline__ float sum8(u32x4 x)
+// Hidden values of a 16-row tile in LDS.  Sixteen lanes read a row's 128
+// values of a step (256 contiguous bytes: consecutive lanes in other rows would
+// cost the address unit four times as much), lane n the chunk n of 8 of them,
+// which lane (row, g = n % 4) of product n / 4 takes.  A chunk's 16 slots are
+// turned by its number, so that writes and reads meet all banks.
+__device__ __forceinline__ int x_slot(int chunk, int row) { return chunk * 16 + (row ^ chunk); }
+
+// INT4: -24 times the sum of a product's 32 values of a row, in the lanes that
+// hold its four chunks.
+__device__ __forceinline__ float x_offset(u32x4 x)
 {
+    const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s += __uint_as_float(x[i] << 16) + __uint_as_float(x[i] & 0xffff0000u);
-    return s;
+    for (int i = 0; i < 4; ++i) {
+        const unsigned two = x[i]; // (a vector's element itself does not cast: the compiler takes element 0)
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), ones, s, false);
+    }
+    s += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(s), 0xb1, 0xf, 0xf, true)); // lane ^ 1
+    s += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(s), 0x4e, 0xf, 0xf, true)); // lane ^ 2
+    return -24.0f * s;
+}
+
+// Few rows, or few vocabulary rows: one workgroup of kRowWaves wavefronts per
+// strip and 16 hidden rows.  The wavefronts take the strip's steps in turn, so
+// that the workgroup reads kRowWaves blocks, one after the other in memory, at
+// a time, and join their sums at the end.  Bound by the weights' HBM bytes: 6.8
+// TB/s at one row, V = 129280, H = 7168, FP4 (72 us).  Eight wavefronts with
+// one step's loads each beat four with two steps' (the registers of the second
+// leave fewer wavefronts) by 1 to 15%.  INT4's scales go through LDS, since a
+// lane needs those of 16 rows (as loads from memory, they cost the address unit
+// more than the weights: 65 us instead of 55 for one row at V = 129280, H =
+// 4096, group 32).
+constexpr int kRowWaves = 8;
+
+template <int FMT, int GROUPS, typename OUT>
+__global__ __launch_bounds__(64 * kRowWaves) void sv_head_rows_kernel(Head q)
+{
+    typedef unsigned short sraw __attribute__((ext_vector_type(GROUPS)));
+    typedef float sfloat __attribute__((ext_vector_type(GROUPS)));
+    __shared__ f32x4 part[kRowWaves][4][64]; // a wavefront's own until the sums are joined
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const long long strip = blockIdx.x % q.nstrip;
+    const int m = (int)(blockIdx.x / q.nstrip) * 16 + c;
+    const unsigned short* row = q.x + (long long)m * q.xs;
+    const bool there = m < q.M;
+    const Int4Bits bits;
+    bf16x8 ones;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ones[k] = (__bf16)1.0f;
+    f32x4 acc[4] = {};
+
+    for (int step = wave; step < q.y.steps; step += kRowWaves) {
+        const long long block = strip * q.y.steps + step;
+        u32x4 w[4], x[4], s4;
+        sraw s2;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = __builtin_nontemporal_load((const u32x4*)(q.packed + block * 4096 + t * 1024 + lane * 16));
+        if constexpr (FMT == SV_W4_FP4) s4 = __builtin_nontemporal_load((const u32x4*)(q.packed + q.y.scale_at + block * 256 + c * 16));
+        else s2 = __builtin_nontemporal_load((const sraw*)(q.packed + q.y.scale_at + block * (GROUPS * 128)) + lane);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int k = step * kStep + 32 * p + 8 * g;
+            x[p] = u32x4{0, 0, 0, 0};
+            if (there && k < q.y.H) x[p] = *(const u32x4_any*)(row + k);
+        }
+        if constexpr (FMT == SV_W4_FP4) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_fp4(w[t][p], fp4_scale(s4[t], p)), __builtin_bit_cast(bf16x8, x[p]), acc[t], 0, 0, 0);
+        } else {
+            sfloat f;
+#pragma unroll
+            for (int i = 0; i < GROUPS; ++i) f[i] = __uint_as_float((unsigned)s2[i] << 16);
+            f32x4* scales = part[wave][0]; // of the step's groups, in vocabulary order
+            wave_sync();
+            ((sfloat*)scales)[lane] = f;
+            wave_sync();
+            constexpr int P = 4 / GROUPS; // products of a group
+#pragma unroll
+            for (int u = 0; u < GROUPS; ++u) {
+                f32x4 sum = {}; // of x over the group, in every row
+#pragma unroll
+                for (int p = u * P; p < u * P + P; ++p)
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, __builtin_bit_cast(bf16x8, x[p]), sum, 0, 0, 0);
+                sum *= -24.0f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    f32x4 d = sum;
+#pragma unroll
+                    for (int p = u * P; p < u * P + P; ++p)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bits.widen(w[t][p]), __builtin_bit_cast(bf16x8, x[p]), d, 0, 0, 0);
+                    add_scaled(acc[t], d, scales[u * 16 + g * 4 + t]);
+                }
+            }
+        }
+    }
+    wave_sync();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) part[wave][t][lane] = acc[t];
+    __syncthreads();
+    if (wave >= 4) return;
+    f32x4 sum = part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) sum += part[w][wave][lane];
+    const long long v = strip * kStrip + 16 * g + 4 * wave;
+    if (there && v < q.y.V) put4((OUT*)q.out + (long long)m * q.os + v, sum, (int)min(4ll, q.y.V - v));
 }
 
 // More rows: a workgroup computes 256 vocabulary rows, a strip to each of its
-// four wavefronts, for 16 MT hidden rows, which they share through LDS.  Each
-// step's hidden values are staged one step ahead, in the order in which the
-// products take them (a wavefront stages product p = its number of every tile,
-// so that both its LDS writes and all reads are contiguous); the weights go
-// straight to the registers of the wavefront that needs them.
+// four wavefronts, for 16 MT hidden rows, which they share through LDS.  The
+// hidden values are staged one step ahead and asked for one step before that;
+// the weights go straight to the registers of the wavefront that needs them,
+// two steps ahead, and are widened between the products, where the vector unit
+// has time.
 template <int FMT, int GROUPS, int MT, typename OUT>
 __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
 {
-    __shared__ u32x4 xt[2][MT][4][64];
-    __shared__ float xsum[2][MT][4][16]; // INT4: -24 times the sum of a product's hidden values
+    typedef unsigned short sraw __attribute__((ext_vector_type(GROUPS)));
+    typedef float sfloat __attribute__((ext_vector_type(GROUPS)));
+    __shared__ u32x4 xt[2][MT][256];
+    __shared__ f32x4 offset[2][FMT == SV_W4_INT4 ? 16 * MT : 1];              // of a row's four products
+    __shared__ f32x4 scales[FMT == SV_W4_INT4 ? 4 : 1][GROUPS * 16]; // of the wavefront's groups, in vocabulary order
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // Workgroups go round the eight dies: the row blocks of one strip group
@@ -331,100 +349,144 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
     const unsigned group = turn / q.nblock * 8 + die;
     if (group * 4ll >= q.y.strips) return;
     const int m0 = (int)(turn % q.nblock) * (16 * MT);
-    const int tiles = min(MT, (q.M - m0 + 15) / 16);
     const long long strip = min(group * 4ll + wave, q.y.strips - 1); // past the last: computed, not stored
-    const long long first = strip * q.y.steps;
+    const int steps = q.y.steps;
+    const unsigned char* wp = q.packed + strip * steps * 4096;
+    const unsigned char* sp = q.packed + q.y.scale_at + strip * steps * (FMT == SV_W4_FP4 ? 256 : GROUPS * 128);
+    const Int4Bits bits;
 
-    u32x4 xr[MT];
-    auto load_x = [&](int step) {
-        const int k = step * kStep + 32 * wave + 8 * g;
+    // staging: chunk n of row r0 of every tile.  Rows past the last are read
+    // from the last (and not stored), values past the hidden size from the last
+    // values (which meet weights or scales of zero).
+    const int n = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    const unsigned short* row[MT];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int m = m0 + 16 * mt + c;
-            xr[mt] = u32x4{0, 0, 0, 0};
-            if (m < q.M && k < q.y.H) xr[mt] = *(const u32x4_any*)(q.x + (long long)m * q.xs + k);
-        }
+    for (int mt = 0; mt < MT; ++mt) row[mt] = q.x + (long long)min(m0 + r0 + 16 * mt, q.M - 1) * q.xs;
+    u32x4 xr[MT], w[2][4], s4[2];
+    sraw s2[2];
+    auto load_x = [&](int step) {
+        const unsigned k = (unsigned)min(step * kStep + 8 * n, q.y.H - 8);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) xr[mt] = *(const u32x4_any*)(row[mt] + k);
     };
     auto stage_x = [&](int buf) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            xt[buf][mt][wave][lane] = xr[mt];
+            xt[buf][mt][x_slot(n, r0)] = xr[mt];
             if constexpr (FMT == SV_W4_INT4) {
-                float s = sum8(xr[mt]);
-                s += __shfl_xor(s, 16);
-                s += __shfl_xor(s, 32);
-                if (g == 0) xsum[buf][mt][wave][c] = -24.0f * s;
+                const float z = x_offset(xr[mt]);
+                if ((n & 3) == 0) ((float*)&offset[buf][16 * mt + r0])[n >> 2] = z;
             }
         }
     };
-    u32x4 w[4], s[FMT == SV_W4_INT4 ? 2 * GROUPS : 1];
-    auto load_w = [&](int step) {
-        const long long block = first + step;
+    auto load_w = [&](int step, int j) { // past the end: the last step again, not used
+        const long long at = min(step, steps - 1);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = *(const u32x4*)(q.packed + block * 4096 + t * 1024 + lane * 16);
-        if constexpr (FMT == SV_W4_FP4) {
-            s[0] = *(const u32x4*)(q.packed + q.y.scale_at + block * 256 + c * 16);
-        } else {
-            const unsigned char* sp = q.packed + q.y.scale_at + block * (GROUPS * 128) + g * 32;
-#pragma unroll
-            for (int u = 0; u < GROUPS; ++u) {
-                s[2 * u] = *(const u32x4*)(sp + u * 128);
-                s[2 * u + 1] = *(const u32x4*)(sp + u * 128 + 16);
-            }
-        }
+        for (int t = 0; t < 4; ++t) w[j][t] = *(const u32x4*)(wp + at * 4096 + t * 1024 + lane * 16);
+        if constexpr (FMT == SV_W4_FP4) s4[j] = *(const u32x4*)(sp + at * 256 + c * 16);
+        else s2[j] = ((const sraw*)(sp + at * (GROUPS * 128)))[lane];
     };
-
     f32x4 acc[MT][4] = {};
-    load_x(0);
-    load_w(0);
-    stage_x(0);
-    if (q.y.steps > 1) load_x(1);
-    for (int step = 0; step < q.y.steps; ++step) {
-        const int buf = step & 1;
-        u32x4 wn[4], sn[FMT == SV_W4_INT4 ? 2 * GROUPS : 1];
+    auto take = [&](int step, int j) { // step's products; j = step % 2
+        if constexpr (FMT == SV_W4_INT4) {
+            sfloat f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) wn[t] = w[t];
-#pragma unroll
-        for (int u = 0; u < (FMT == SV_W4_INT4 ? 2 * GROUPS : 1); ++u) sn[u] = s[u];
-        lds_barrier();
-        if (step + 1 < q.y.steps) {
-            load_w(step + 1);
-            stage_x(buf ^ 1);
-            if (step + 2 < q.y.steps) load_x(step + 2);
+            for (int i = 0; i < GROUPS; ++i) f[i] = __uint_as_float((unsigned)s2[j][i] << 16);
+            ((sfloat*)scales[wave])[lane] = f;
         }
-        constexpr int P = 4 / GROUPS; // products of a group (INT4)
-        f32x4 d[FMT == SV_W4_INT4 ? MT : 1][4];
+        lds_barrier();
+        stage_x(j ^ 1);
+        load_x(step + 2);
+        auto hidden = [&](int mt, int p) { return __builtin_bit_cast(bf16x8, xt[j][mt][x_slot(4 * p + g, c)]); };
+        if constexpr (FMT == SV_W4_FP4) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            bf16x8 a[4];
+            for (int p = 0; p < 4; ++p) {
+                bf16x8 a[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                a[t] = FMT == SV_W4_FP4 ? widen_fp4(wn[t][p], fp4_scale(sn[0][t], p)) : widen_int4(wn[t][p]);
+                for (int t = 0; t < 4; ++t) a[t] = widen_fp4(w[j][t][p], fp4_scale(s4[j][t], p));
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (mt >= tiles) continue;
-                const bf16x8 b = __builtin_bit_cast(bf16x8, xt[buf][mt][p][lane]);
-                if constexpr (FMT == SV_W4_FP4) {
+                for (int mt = 0; mt < MT; ++mt) {
+                    const bf16x8 b = hidden(mt, p);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) acc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t], b, acc[mt][t], 0, 0, 0);
-                } else {
-                    if (p % P == 0) {
-                        float z = xsum[buf][mt][p][c];
+                }
+            }
+        } else if constexpr (GROUPS == 1) {
+            f32x4 d[MT][4];
 #pragma unroll
-                        for (int o = 1; o < P; ++o) z += xsum[buf][mt][p + o][c];
+            for (int p = 0; p < 4; ++p) {
+                bf16x8 a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = bits.widen(w[j][t][p]);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const bf16x8 b = hidden(mt, p);
+                    if (p == 0) {
+                        const f32x4 z4 = offset[j][16 * mt + c];
+                        const float z = (z4[0] + z4[1]) + (z4[2] + z4[3]);
 #pragma unroll
                         for (int t = 0; t < 4; ++t) d[mt][t] = f32x4{z, z, z, z};
                     }
 #pragma unroll
                     for (int t = 0; t < 4; ++t) d[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t], b, d[mt][t], 0, 0, 0);
-                    if (p % P == P - 1) {
+                    if (p == 3) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) add_scaled(acc[mt][t], d[mt][t], sn[2 * (p / P) + t / 2], t);
+                        for (int t = 0; t < 4; ++t) add_scaled(acc[mt][t], d[mt][t], scales[wave][g * 4 + t]);
+                    }
+                }
+            }
+        } else {
+            constexpr int P = 4 / GROUPS; // products of a group
+#pragma unroll
+            for (int u = 0; u < GROUPS; ++u) {
+                bf16x8 a[P][4];
+                f32x4 s[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        unsigned word = w[j][t][u * P + p];
+                        asm volatile("" : "+v"(word) : : "memory");
+                        a[p][t] = bits.widen(word);
+                    }
+                    s[t] = scales[wave][u * 16 + g * 4 + t];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const f32x4 z4 = offset[j][16 * mt + c];
+                    const float z = GROUPS == 4 ? z4[u] : z4[2 * u & 3] + z4[(2 * u + 1) & 3];
+                    f32x4 d[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) d[t] = f32x4{z, z, z, z};
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const bf16x8 b = hidden(mt, u * P + p);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][t], b, d[t], 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        add_scaled(acc[mt][t], d[t], s[t]);
+                        asm volatile("" : "+v"(acc[mt][t])); // one tile after the other, or their sums pile up and spill
                     }
                 }
             }
         }
+        load_w(step + 2, j);
+    };
+
+    load_x(0);
+    load_w(0, 0);
+    load_w(1, 1);
+    stage_x(0);
+    load_x(1);
+    int step = 0;
+    for (; step + 2 <= steps; step += 2) {
+        take(step, 0);
+        take(step + 1, 1);
     }
+    if (step < steps) take(step, 0);
+
     if (group * 4ll + wave >= q.y.strips) return;
     const long long v = strip * kStrip + 16 * g;
 #pragma unroll
@@ -434,7 +496,7 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
         OUT* out = (OUT*)q.out + (long long)m * q.os + v;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            if (v + 4 * t < q.y.V) put4(out + 4 * t, acc[mt][t], (int)(q.y.V - v - 4 * t));
+            if (v + 4 * t < q.y.V) put4(out + 4 * t, acc[mt][t], (int)min(4ll, q.y.V - v - 4 * t));
     }
 }
 
@@ -446,48 +508,67 @@ int check_weights(int32_t hidden, int32_t format, int32_t group)
     return SV_OK;
 }
 
-template <int FMT, int GROUPS, int WK>
-hipError_t launch_rows(Head q, bool bf16, hipStream_t s)
+// Launches of at most 2^32 - 1 work-items: `per` workgroups of `threads` for
+// each block of `rows` hidden rows.
+template <typename Launch>
+hipError_t in_launches(Head q, long long per, int threads, int rows, int es, Launch launch)
+{
+    const int most = (int)std::min(0xffffffffll / threads / per, (long long)(1 << 30) / rows) * rows;
+    for (int left = q.M; left > 0; left -= most) {
+        q.M = std::min(left, most);
+        q.nblock = (unsigned)((q.M + rows - 1) / rows);
+        const hipError_t e = launch(q, dim3((unsigned)(per * q.nblock)), dim3(threads));
+        if (e != hipSuccess) return e;
+        q.x += (long long)most * q.xs;
+        q.out = (char*)q.out + (long long)most * q.os * es;
+    }
+    return hipSuccess;
+}
+
+template <int FMT, int GROUPS, typename OUT>
+hipError_t launch_rows(Head q, hipStream_t s)
 {
     q.nstrip = (unsigned)q.y.strips;
-    // launches of at most 2^32 - 1 work-items
-    const int most = (int)std::min(0xffffffffll / (64 * WK) / q.nstrip, 1ll << 24) * 16;
-    hipError_t e = hipSuccess;
-    for (int left = q.M; left > 0 && e == hipSuccess; left -= most) {
-        q.M = std::min(left, most);
-        const dim3 grid(q.nstrip * (unsigned)((q.M + 15) / 16));
-        if (bf16) e = launch_kernel(sv_head_rows_kernel<FMT, GROUPS, WK, __bf16>, grid, dim3(64 * WK), 0, s, nullptr, nullptr, q);
-        else e = launch_kernel(sv_head_rows_kernel<FMT, GROUPS, WK, float>, grid, dim3(64 * WK), 0, s, nullptr, nullptr, q);
-        q.x += (long long)most * q.xs;
-        q.out = (char*)q.out + (long long)most * q.os * (bf16 ? 2 : 4);
-    }
-    return e;
+    return in_launches(q, q.y.strips, 64 * kRowWaves, 16, sizeof(OUT), [&](const Head& a, dim3 grid, dim3 block) {
+        return launch_kernel(sv_head_rows_kernel<FMT, GROUPS, OUT>, grid, block, 0, s, nullptr, nullptr, a);
+    });
 }
 
-template <int FMT, int GROUPS, int MT>
-hipError_t launch_tile(Head q, bool bf16, hipStream_t s)
+template <int FMT, int GROUPS, int MT, typename OUT>
+hipError_t launch_tile(const Head& q, hipStream_t s)
 {
-    const long long groups = ((q.y.strips + 3) / 4 + 7) / 8 * 8;
-    const int most = (int)std::min(0xffffffffll / 256 / groups, 1ll << 22) * (16 * MT);
-    hipError_t e = hipSuccess;
-    for (int left = q.M; left > 0 && e == hipSuccess; left -= most) {
-        q.M = std::min(left, most);
-        q.nblock = (unsigned)((q.M + 16 * MT - 1) / (16 * MT));
-        const dim3 grid((unsigned)(groups * q.nblock));
-        if (bf16) e = launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, __bf16>, grid, dim3(256), 0, s, nullptr, nullptr, q);
-        else e = launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, float>, grid, dim3(256), 0, s, nullptr, nullptr, q);
-        q.x += (long long)most * q.xs;
-        q.out = (char*)q.out + (long long)most * q.os * (bf16 ? 2 : 4);
-    }
-    return e;
+    return in_launches(q, ((q.y.strips + 3) / 4 + 7) / 8 * 8, 256, 16 * MT, sizeof(OUT), [&](const Head& a, dim3 grid, dim3 block) {
+        return launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, OUT>, grid, block, 0, s, nullptr, nullptr, a);
+    });
 }
 
-template <int FMT, int GROUPS>
-hipError_t launch_head(const Head& q, bool bf16, hipStream_t s)
+template <int FMT, int GROUPS, typename OUT>
+hipError_t launch_head(const Head& q, hipStream_t s)
 {
-    if (q.M <= 16) return launch_rows<FMT, GROUPS, 4>(q, bf16, s);
-    if (q.M <= 32) return launch_tile<FMT, GROUPS, 2>(q, bf16, s);
-    return launch_tile<FMT, GROUPS, 4>(q, bf16, s);
+    // A tile workgroup does the work of four strips for 16 MT rows but takes the
+    // same time however few of them there are (measured: about 1 us a step for
+    // FP4, 1.5 to 2.5 for INT4 of group 128 to 32, at MT = 4), while the row
+    // workgroups, 4 MT times as many, do 1050 steps of a strip and 16 rows a us on
+    // the whole chip whatever their number.  So the tiles need enough workgroups:
+    // 64 rows at V = 8000, H = 4096 FP4 take 32 us as tiles and 19 as rows, at V =
+    // 50257 43 and 100; 64 rows at V = 32000 INT4 of group 32 take 83 and 65.  Up
+    // to 8 rows the weights' bytes bound both, and the rows read them faster (one
+    // row at V = 129280, H = 7168: 76 and 87 us).
+    const int mt = q.M <= 16 ? 1 : q.M <= 32 ? 2 : 4;
+    const long long tiles = (q.y.strips + 3) / 4 * ((q.M + 16 * mt - 1) / (16 * mt)) * mt;
+    if (q.M <= 8 || tiles < (FMT == SV_W4_FP4 ? 256 : 640)) return launch_rows<FMT, GROUPS, OUT>(q, s);
+    if (mt == 1) return launch_tile<FMT, GROUPS, 1, OUT>(q, s);
+    if (mt == 2) return launch_tile<FMT, GROUPS, 2, OUT>(q, s);
+    return launch_tile<FMT, GROUPS, 4, OUT>(q, s);
+}
+
+template <typename OUT>
+hipError_t launch_format(const Head& q, int format, int group, hipStream_t s)
+{
+    if (format == SV_W4_FP4) return launch_head<SV_W4_FP4, 4, OUT>(q, s);
+    if (group == 32) return launch_head<SV_W4_INT4, 4, OUT>(q, s);
+    if (group == 64) return launch_head<SV_W4_INT4, 2, OUT>(q, s);
+    return launch_head<SV_W4_INT4, 1, OUT>(q, s);
 }
 
 } // namespace
@@ -569,12 +650,8 @@ int spec_verify_head(spec_verify_t* h, const spec_verify_head_args* a, void* hip
     q.out = a->logits;
     q.os = a->logits_stride;
     q.nstrip = q.nblock = 0;
-    const bool bf16 = cfg->dtype == SV_BF16;
-    hipError_t e;
-    if (a->format == SV_W4_FP4) e = launch_head<SV_W4_FP4, 4>(q, bf16, s);
-    else if (a->group == 32) e = launch_head<SV_W4_INT4, 4>(q, bf16, s);
-    else if (a->group == 64) e = launch_head<SV_W4_INT4, 2>(q, bf16, s);
-    else e = launch_head<SV_W4_INT4, 1>(q, bf16, s);
+    const hipError_t e = cfg->dtype == SV_BF16 ? launch_format<__bf16>(q, a->format, a->group, s)
+                                               : launch_format<float>(q, a->format, a->group, s);
     return e == hipSuccess ? SV_OK : SV_EDEVICE;
 }
 

@@ -107,6 +107,13 @@ CASES = [
     (4, 300, 256, "fp4", 32, "bf16", dict(xpad=8, lpad=5)), (4, 300, 256, "int4", 64, "f32", dict(xpad=3, xshift=1, lpad=1, lshift=3)),
     (70, 130, 288, "fp4", 32, "bf16", dict(xpad=1, xshift=5, lshift=1, lpad=2)), (1, 129280, 1024, "fp4", 32, "bf16", {}),
     (600, 2000, 128, "int4", 32, "f32", {}),
+    # enough vocabulary and rows for the tiles of 16, 32 and 64 rows, over an odd and an even number of steps
+    (9, 65700, 160, "fp4", 32, "f32", {}), (16, 65601, 352, "fp4", 32, "bf16", dict(xpad=1, xshift=3, lshift=1)),
+    (12, 164000, 192, "int4", 64, "f32", {}), (16, 164100, 128, "int4", 128, "bf16", {}), (13, 164099, 96, "int4", 32, "f32", {}),
+    (20, 33001, 288, "fp4", 32, "f32", {}), (31, 82100, 320, "int4", 64, "bf16", {}), (32, 82001, 384, "int4", 128, "f32", {}),
+    (17, 82100, 160, "int4", 32, "f32", dict(xpad=8, lpad=3)), (64, 20000, 416, "fp4", 32, "f32", {}), (40, 20033, 128, "fp4", 32, "bf16", {}),
+    (130, 20001, 640, "int4", 128, "f32", {}), (129, 20001, 192, "int4", 64, "bf16", dict(xpad=3, lpad=1)),
+    (190, 20001, 160, "int4", 32, "f32", {}),
 ]
 
 
@@ -147,10 +154,10 @@ def test_nan_scale_reaches_its_row_only():
     assert np.isnan(got[:, 77]).all() and np.isfinite(np.delete(got, 77, 1)).all()
 
 
-@pytest.mark.parametrize("fmt", ["fp4", "int4"])
-def test_rows_do_not_depend_on_each_other(fmt):
-    wt = Weights(1000, 512, fmt, 32, seed=6)
-    x = _x(np.random.default_rng(7), 40, 512)
+@pytest.mark.parametrize("fmt,V,H", [("fp4", 1000, 512), ("int4", 1000, 512), ("fp4", 20000, 160), ("int4", 50000, 160)])
+def test_rows_do_not_depend_on_each_other(fmt, V, H):
+    wt = Weights(V, H, fmt, 32, seed=6)
+    x = _x(np.random.default_rng(7), 40, H)
     got, raw = _run(wt, x, "f32")
     again, _ = _run(wt, x, "f32")
     assert np.array_equal(got, again)

@@ -477,6 +477,18 @@ __global__ __launch_bounds__(kThreads) void sv_history_clear_kernel(Hist q)
     for (int v = part * kThreads + threadIdx.x; v < q.words; v += q.per * kThreads) s[v] = 0;
 }
 
+// A token of sequence b's list, or -1 (padding, or an id that is reported and
+// left out).
+__device__ __forceinline__ int token_at(const Hist& q, long long i)
+{
+    const int v = q.tok[i];
+    if ((unsigned)v < (unsigned)q.V) return v;
+    if (v != -1) bad_input(q.status);
+    return -1;
+}
+
+// One token to a thread, with an atomic on its word of the seen bits and one on
+// its count.  Bound by those atomics, about 17 to a ns over the whole chip.
 __global__ __launch_bounds__(kThreads) void sv_history_add_kernel(Hist q)
 {
     const int b = blockIdx.x / q.per, part = blockIdx.x % q.per;
@@ -487,14 +499,46 @@ __global__ __launch_bounds__(kThreads) void sv_history_add_kernel(Hist q)
     int* c = q.counts + (long long)slot * q.V;
     unsigned* s = q.seen + (long long)slot * q.words;
     for (int i = part * kThreads + threadIdx.x; i < n; i += q.per * kThreads) {
-        const int v = q.tok[first + i];
-        if (v == -1) continue;
-        if ((unsigned)v >= (unsigned)q.V) {
-            bad_input(q.status);
-            continue;
-        }
+        const int v = token_at(q, first + i);
+        if (v < 0) continue;
         __hip_atomic_fetch_or(s + (v >> 5), 1u << (v & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (q.kind == SV_HISTORY_OUTPUT) __hip_atomic_fetch_add(c + v, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+// Long lists: a workgroup gathers the seen bits of its part of a list in LDS and
+// adds them to the slot's word by word, where consecutive lanes meet
+// consecutive words.  A range of kBitWords words at a time (all of them up to
+// a vocabulary of 524288).
+constexpr int kBitThreads = 1024;
+constexpr int kBitWords = 16384;
+
+__global__ __launch_bounds__(kBitThreads) void sv_history_bits_kernel(Hist q)
+{
+    extern __shared__ unsigned bits[];
+    const int b = blockIdx.x / q.per, part = blockIdx.x % q.per;
+    long long first;
+    int n;
+    const int slot = hist_seq(q, b, first, n, part == 0 && threadIdx.x == 0);
+    if (slot < 0) return;
+    int* c = q.counts + (long long)slot * q.V;
+    unsigned* s = q.seen + (long long)slot * q.words;
+    const int share = (n + q.per - 1) / q.per, i0 = part * share, i1 = min(n, i0 + share);
+    if (i0 >= i1) return;
+    for (int w0 = 0; w0 < q.words; w0 += kBitWords) {
+        const int words = min(kBitWords, q.words - w0);
+        for (int w = threadIdx.x; w < words; w += kBitThreads) bits[w] = 0;
+        __syncthreads();
+        for (int i = i0 + threadIdx.x; i < i1; i += kBitThreads) {
+            const int v = token_at(q, first + i), w = (v >> 5) - w0;
+            if (v < 0 || (unsigned)w >= (unsigned)words) continue;
+            __hip_atomic_fetch_or(bits + w, 1u << (v & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            if (q.kind == SV_HISTORY_OUTPUT) __hip_atomic_fetch_add(c + v, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        for (int w = threadIdx.x; w < words; w += kBitThreads)
+            if (bits[w]) __hip_atomic_fetch_or(s + w0 + w, bits[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
     }
 }
 
@@ -669,7 +713,15 @@ int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, voi
         e = launch_kernel(sv_history_clear_kernel, dim3((unsigned)((long long)q.B * q.per)), dim3(kThreads), 0, s, nullptr,
                           nullptr, q);
     }
-    if (e == hipSuccess) {
+    // The bits in LDS cost a workgroup about 5 us whatever the list, so they are for
+    // long lists, and where the atomics would take longer than that: 256 lists of
+    // up to 8192 tokens take 8 us with them and 95 without.
+    if (e == hipSuccess && q.most >= 512 && (long long)q.B * q.most >= 32768) {
+        q.per = (int)std::min(cap / 4, std::min(64ll, (q.most + 8191ll) / 8192));
+        const size_t lds = sizeof(unsigned) * std::min(kBitWords, q.words);
+        e = launch_kernel(sv_history_bits_kernel, dim3((unsigned)((long long)q.B * q.per)), dim3(kBitThreads), (uint32_t)lds, s,
+                          nullptr, nullptr, q);
+    } else if (e == hipSuccess) {
         q.per = std::min(64, parts(q.most));
         e = launch_kernel(sv_history_add_kernel, dim3((unsigned)((long long)q.B * q.per)), dim3(kThreads), 0, s, nullptr,
                           nullptr, q);

@@ -173,6 +173,18 @@ struct Listed {
     unsigned short at[SPAN];          // the touched tokens, ascending
 };
 
+// Element i of an array that may not be given.  The load is unconditional, so
+// that several of them are under way together.
+struct Given {
+    const char* any = (const char*)__builtin_amdgcn_kernarg_segment_ptr();
+    template <typename T>
+    __device__ __forceinline__ T operator()(const T* p, long long i, T otherwise) const
+    {
+        const T v = *(p ? p + i : (const T*)any);
+        return p ? v : otherwise;
+    }
+};
+
 // What the wavefronts of a workgroup have left alive of its rows.
 struct Tally {
     int live[64]; // of row r0 + i
@@ -199,11 +211,38 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     const bool teller = w0 == 0;         // the wavefront that reports what the sequence brings
     const bool tells = teller && lane == 0;
 
+    // What the sequence brings, asked for all at once (an array that is not
+    // given reads the kernel's arguments, and its value is not used): a call of
+    // one row takes as long as its chain of dependent loads.
+    const Given give;
     long long first;
     const int n = rows_of(q, b, first);
+    const int given_slot = give(q.slots, b, b);
+    float rep = give(q.rep, b, 1.0f), freq = give(q.freq, b, 0.0f), pres = give(q.pres, b, 0.0f);
+    int e0 = give(q.boff, b, 0), e1 = give(q.boff, b + 1, 0);
+    const int far = min(q.chunk, q.rows - r0); // rows of the chunk, if the sequence has them all
+    int my_mask = -1, my_draft = -1, draft0 = -1;
+    if (q.masks && lane < far) my_mask = q.midx[(long long)b * q.rows + r0 + lane];
+    const int* draft = q.draft + b * q.dstride;
+    if (q.draft && lane + 1 < far) my_draft = draft[q.row0 + r0 + lane]; // between row lane and the next
+    if (q.draft && lane < q.row0 + r0 + far - 1) draft0 = draft[lane];
+
     if (tells && r0 == 0 && n < 0) bad_input(q.status);
     if (r0 >= n) return;
     const int r1 = min(r0 + q.chunk, n); // at most 64 rows: a lane's share of what each row brings
+    if (r0 + lane >= r1) my_mask = -1;
+    if (r0 + lane + 1 >= r1) my_draft = -1;
+    int slot = q.counts ? given_slot : -1;
+    const bool slot_ok = slot >= -1 && slot < q.n_slots;
+    const bool rep_ok = rep > 0.0f && rep < INFINITY, freq_ok = fabsf(freq) < INFINITY, pres_ok = fabsf(pres) < INFINITY;
+    const bool bias_ok = e0 >= 0 && e0 <= e1 && e1 <= q.n_biases;
+    if (tells && !((slot_ok || !q.counts) && rep_ok && freq_ok && pres_ok && (bias_ok || !q.boff))) bad_input(q.status);
+    if (teller && q.masks && (my_mask < -1 || my_mask >= q.n_masks)) bad_input(q.status);
+    if (!slot_ok) slot = -1;
+    if (!rep_ok) rep = 1.0f;
+    if (!freq_ok) freq = 0.0f;
+    if (!pres_ok) pres = 0.0f;
+    if (!bias_ok) e0 = e1 = 0;
 
     const elem* src = (const elem*)q.in + (q.roff ? (first + r0) * q.irs : b * q.ibs + r0 * q.irs) + v0;
     elem* dst = (elem*)q.out + (q.roff ? (first + r0) * q.ors : b * q.obs + r0 * q.ors) + w0;
@@ -215,13 +254,14 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     auto fetch = [&](int i, raw& xr) {
         if (r0 + i < r1 && inside) xr = load_logits<DT>(src + i * q.irs, v0, q.V);
     };
-    if (!INPLACE) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) fetch(u, x[u]);
+    unsigned mine = 0; // the lane's touched tokens
+    if (slot >= 0 && inside) mine = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
+    int bias_tok = -1;
+    float bias_val = 0.0f;
+    if (e0 + lane < e1) {
+        bias_tok = q.btok[e0 + lane];
+        bias_val = q.bval[e0 + lane];
     }
-    const int my_mask = q.masks && r0 + lane < r1 ? q.midx[(long long)b * q.rows + r0 + lane] : -1;
-    const int my_draft = q.draft && r0 + lane + 1 < r1 ? q.draft[b * q.dstride + q.row0 + r0 + lane] : -1;
-    if (teller && (my_mask < -1 || my_mask >= q.n_masks) && q.masks) bad_input(q.status);
     auto mask_of = [&](int i) { return __builtin_amdgcn_readlane(my_mask, i); }; // of row r0 + i, i < 64
     auto fetch_mask = [&](int i, unsigned& al) {
         al = ALL;
@@ -233,30 +273,15 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fetch_mask(u, allow[u]);
+    if (!INPLACE) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) fetch(u, x[u]);
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fetch_mask(u + kAhead, allow_next[u]);
 
-    int slot = -1;
-    if (q.counts) {
-        slot = q.slots ? q.slots[b] : b;
-        if (slot < -1 || slot >= q.n_slots) {
-            if (tells) bad_input(q.status);
-            slot = -1;
-        }
-    }
-    float rep = q.rep ? q.rep[b] : 1.0f, freq = q.freq ? q.freq[b] : 0.0f, pres = q.pres ? q.pres[b] : 0.0f;
-    const bool rep_ok = rep > 0.0f && rep < INFINITY, freq_ok = fabsf(freq) < INFINITY, pres_ok = fabsf(pres) < INFINITY;
-    if (tells && !(rep_ok && freq_ok && pres_ok)) bad_input(q.status);
-    if (!rep_ok) rep = 1.0f;
-    if (!freq_ok) freq = 0.0f;
-    if (!pres_ok) pres = 0.0f;
-
     // history
-    unsigned mine = 0; // the lane's touched tokens
-    if (slot >= 0 && inside) {
-        mine = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
-        if (v0 + PT > q.V) mine &= (1u << (q.V - v0)) - 1;
-    }
+    if (v0 + PT > q.V) mine &= inside ? (1u << (q.V - v0)) - 1 : 0u;
     {
         const int* c = q.counts + (long long)slot * q.V + v0;
 #pragma unroll
@@ -277,9 +302,9 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     };
     for (int i0 = 0; i0 < j1; i0 += 64) {
         const int i = i0 + lane;
-        const int x = i < j1 ? q.draft[b * q.dstride + i] : 0;
+        const int x = i0 == 0 ? draft0 : i < j1 ? draft[i] : -1;
         const bool fine = (unsigned)x < (unsigned)q.V;
-        if (teller && !fine) bad_input(q.status);
+        if (teller && i < j1 && !fine) bad_input(q.status);
         unsigned long long hit = __ballot(i < j1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
         while (hit) {
             const int src = __builtin_ctzll(hit);
@@ -290,24 +315,23 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
         }
     }
     // biases, likewise, added in the list's order
-    if (q.boff) {
-        int e0 = q.boff[b], e1 = q.boff[b + 1];
-        if (e0 < 0 || e1 < e0 || e1 > q.n_biases) {
-            if (tells) bad_input(q.status);
-            e0 = e1 = 0;
+    for (int i0 = e0; i0 < e1; i0 += 64) {
+        const int x = bias_tok, left = e1 - i0;
+        const float val = bias_val;
+        if (i0 + 64 + lane < e1) {
+            bias_tok = q.btok[i0 + 64 + lane];
+            bias_val = q.bval[i0 + 64 + lane];
         }
-        for (int i0 = e0; i0 < e1; i0 += 64) {
-            const int x = q.btok[min(i0 + lane, e1 - 1)];
-            const bool fine = (unsigned)x < (unsigned)q.V;
-            if (teller && !fine) bad_input(q.status);
-            unsigned long long hit = __ballot(i0 + lane < e1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
-            while (hit) {
-                const int src = __builtin_ctzll(hit);
-                hit &= hit - 1;
-                const int y = __builtin_amdgcn_readlane(x, src) - w0;
-                if (y / PT == lane) mine |= 1u << (y % PT);
-                if (lane == 0) s.bias[y] += q.bval[i0 + src];
-            }
+        const bool fine = (unsigned)x < (unsigned)q.V;
+        if (teller && lane < left && !fine) bad_input(q.status);
+        unsigned long long hit = __ballot(lane < left && fine && (unsigned)(x - w0) < (unsigned)SPAN);
+        while (hit) {
+            const int src = __builtin_ctzll(hit);
+            hit &= hit - 1;
+            const int y = __builtin_amdgcn_readlane(x, src) - w0;
+            const float add = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(val), src));
+            if (y / PT == lane) mine |= 1u << (y % PT);
+            if (lane == 0) s.bias[y] += add;
         }
     }
     // the list, in the order of the lanes

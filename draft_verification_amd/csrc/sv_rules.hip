@@ -95,7 +95,35 @@ struct Vec<SV_BF16> {
     static __device__ float get(elem x) { return __uint_as_float((unsigned)x << 16); }
     static __device__ elem put(float x) { return __builtin_bit_cast(elem, (__bf16)x); }
     static __device__ elem none() { return 0xff80; } // -infinity
+
+    // -infinity where the bit is 0, two tokens at a time.
+    static __device__ __forceinline__ void mask(raw& x, unsigned bits)
+    {
+        typedef unsigned pairs __attribute__((ext_vector_type(4)));
+        pairs p = __builtin_bit_cast(pairs, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned lo = (unsigned)((int)(bits << (31 - 2 * i)) >> 31), hi = (unsigned)((int)(bits << (30 - 2 * i)) >> 31);
+            const unsigned keep = (lo & 0xffffu) | (hi & 0xffff0000u);
+            p[i] = (p[i] & keep) | (0xff80ff80u & ~keep);
+        }
+        x = __builtin_bit_cast(raw, p);
+    }
 };
+
+// The sum of a value over a wavefront's lanes.
+__device__ __forceinline__ int wave_total(int v)
+{
+#define SV_ADD(ctrl, rows) v += __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xf, false)
+    SV_ADD(0x111, 0xf); // row shifts by 1, 2, 4, 8
+    SV_ADD(0x112, 0xf);
+    SV_ADD(0x114, 0xf);
+    SV_ADD(0x118, 0xf);
+    SV_ADD(0x142, 0xa); // row 0's and 2's last lane to the next row
+    SV_ADD(0x143, 0xc); // the first half's last lane to the second
+#undef SV_ADD
+    return __builtin_amdgcn_readlane(v, 63);
+}
 
 template <>
 struct Vec<SV_F32> {
@@ -105,6 +133,11 @@ struct Vec<SV_F32> {
     static __device__ float get(elem x) { return x; }
     static __device__ elem put(float x) { return x; }
     static __device__ elem none() { return -INFINITY; }
+    static __device__ __forceinline__ void mask(raw& x, unsigned bits)
+    {
+#pragma unroll
+        for (int k = 0; k < PT; ++k) x[k] = bits >> k & 1 ? x[k] : -INFINITY;
+    }
 };
 
 // A lane's PT bits of a bit row, from token v0 (a multiple of PT).
@@ -280,19 +313,6 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fetch_mask(u + kAhead, allow_next[u]);
 
-    // history
-    if (v0 + PT > q.V) mine &= inside ? (1u << (q.V - v0)) - 1 : 0u;
-    {
-        const int* c = q.counts + (long long)slot * q.V + v0;
-#pragma unroll
-        for (int k = 0; k < PT; ++k) {
-            s.cnt[lane * PT + k] = mine >> k & 1 ? 1 + c[k] : 0;
-            s.bias[lane * PT + k] = 0.0f;
-        }
-    }
-    wave_sync();
-    // drafted tokens, 64 ids at a time, those of the wavefront's span one by
-    // one: the first j0 precede the chunk's first row, the others a later one
     const int j0 = q.draft ? q.row0 + r0 : 0, j1 = q.draft ? q.row0 + r1 - 1 : 0;
     auto add_draft = [&](int y) { // counts token w0 + y once more
         if (lane == 0) {
@@ -300,50 +320,76 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
             s.cnt[y] = c ? c + 1 : 2;
         }
     };
-    for (int i0 = 0; i0 < j1; i0 += 64) {
-        const int i = i0 + lane;
-        const int x = i0 == 0 ? draft0 : i < j1 ? draft[i] : -1;
-        const bool fine = (unsigned)x < (unsigned)q.V;
-        if (teller && i < j1 && !fine) bad_input(q.status);
-        unsigned long long hit = __ballot(i < j1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
-        while (hit) {
-            const int src = __builtin_ctzll(hit);
-            hit &= hit - 1;
-            const int y = __builtin_amdgcn_readlane(x, src) - w0;
-            if (y / PT == lane) mine |= 1u << (y % PT);
-            if (i0 + src < j0) add_draft(y);
-        }
-    }
-    // biases, likewise, added in the list's order
-    for (int i0 = e0; i0 < e1; i0 += 64) {
-        const int x = bias_tok, left = e1 - i0;
-        const float val = bias_val;
-        if (i0 + 64 + lane < e1) {
-            bias_tok = q.btok[i0 + 64 + lane];
-            bias_val = q.bval[i0 + 64 + lane];
-        }
-        const bool fine = (unsigned)x < (unsigned)q.V;
-        if (teller && lane < left && !fine) bad_input(q.status);
-        unsigned long long hit = __ballot(lane < left && fine && (unsigned)(x - w0) < (unsigned)SPAN);
-        while (hit) {
-            const int src = __builtin_ctzll(hit);
-            hit &= hit - 1;
-            const int y = __builtin_amdgcn_readlane(x, src) - w0;
-            const float add = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(val), src));
-            if (y / PT == lane) mine |= 1u << (y % PT);
-            if (lane == 0) s.bias[y] += add;
-        }
-    }
-    // the list, in the order of the lanes
-    int listed = 0, at = 0;
+    int listed = 0; // tokens that any row of the chunk touches
+    if (slot >= 0 || j1 > 0 || e0 < e1) {
+        // history
+        if (v0 + PT > q.V) mine &= inside ? (1u << (q.V - v0)) - 1 : 0u;
+        {
+            typedef int four __attribute__((ext_vector_type(4), aligned(4)));
+            const int* c = q.counts + (long long)slot * q.V + v0;
+            four count[PT / 4] = {};
+            if (mine && v0 + PT <= q.V) {
 #pragma unroll
-    for (int k = 0; k < PT; ++k) {
-        const unsigned long long has = __ballot(mine >> k & 1);
-        listed += __popcll(has);
-        at += __builtin_amdgcn_mbcnt_hi((unsigned)(has >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)has, 0));
+                for (int k = 0; k < PT / 4; ++k) count[k] = ((const four*)c)[k];
+            } else if (mine) {
+#pragma unroll
+                for (int k = 0; k < PT; ++k)
+                    if (mine >> k & 1) count[k / 4][k % 4] = c[k];
+            }
+#pragma unroll
+            for (int k = 0; k < PT; ++k) {
+                s.cnt[lane * PT + k] = mine >> k & 1 ? 1 + count[k / 4][k % 4] : 0;
+                s.bias[lane * PT + k] = 0.0f;
+            }
+        }
+        wave_sync();
+        // drafted tokens, 64 ids at a time, those of the wavefront's span one by
+        // one: the first j0 precede the chunk's first row, the others a later one
+        for (int i0 = 0; i0 < j1; i0 += 64) {
+            const int i = i0 + lane;
+            const int x = i0 == 0 ? draft0 : i < j1 ? draft[i] : -1;
+            const bool fine = (unsigned)x < (unsigned)q.V;
+            if (teller && i < j1 && !fine) bad_input(q.status);
+            unsigned long long hit = __ballot(i < j1 && fine && (unsigned)(x - w0) < (unsigned)SPAN);
+            while (hit) {
+                const int src = __builtin_ctzll(hit);
+                hit &= hit - 1;
+                const int y = __builtin_amdgcn_readlane(x, src) - w0;
+                if (y / PT == lane) mine |= 1u << (y % PT);
+                if (i0 + src < j0) add_draft(y);
+            }
+        }
+        // biases, likewise, added in the list's order
+        for (int i0 = e0; i0 < e1; i0 += 64) {
+            const int x = bias_tok, left = e1 - i0;
+            const float val = bias_val;
+            if (i0 + 64 + lane < e1) {
+                bias_tok = q.btok[i0 + 64 + lane];
+                bias_val = q.bval[i0 + 64 + lane];
+            }
+            const bool fine = (unsigned)x < (unsigned)q.V;
+            if (teller && lane < left && !fine) bad_input(q.status);
+            unsigned long long hit = __ballot(lane < left && fine && (unsigned)(x - w0) < (unsigned)SPAN);
+            while (hit) {
+                const int src = __builtin_ctzll(hit);
+                hit &= hit - 1;
+                const int y = __builtin_amdgcn_readlane(x, src) - w0;
+                const float add = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(val), src));
+                if (y / PT == lane) mine |= 1u << (y % PT);
+                if (lane == 0) s.bias[y] += add;
+            }
+        }
+        // the list, in the order of the lanes
+        int at = 0;
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            const unsigned long long has = __ballot(mine >> k & 1);
+            listed += __popcll(has);
+            at += __builtin_amdgcn_mbcnt_hi((unsigned)(has >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)has, 0));
+        }
+        for (unsigned m = mine; m; m &= m - 1) s.at[at++] = (unsigned short)(lane * PT + __builtin_ctz(m));
+        wave_sync();
     }
-    for (unsigned m = mine; m; m &= m - 1) s.at[at++] = (unsigned short)(lane * PT + __builtin_ctz(m));
-    wave_sync();
 
     const float inv = 1.0f / rep;
     auto apply = [&](float l, int y) { // the rules for token w0 + y
@@ -398,13 +444,14 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
                     wave_sync();
                 }
                 if (masked) {
-                    int live = 0;
+                    X::mask(x[u], allow[u]);
+                    if (q.live) { // lanes and tokens past the row's end are -infinity here
+                        int n = 0;
 #pragma unroll
-                    for (int k = 0; k < PT; ++k) {
-                        if (!(allow[u] >> k & 1)) x[u][k] = X::none();
-                        live += __popcll(__ballot(v0 + k < q.V && X::get(x[u][k]) > -INFINITY));
+                        for (int k = 0; k < PT; ++k) n += X::get(x[u][k]) > -INFINITY;
+                        n = wave_total(n);
+                        if (lane == i) my_live = n;
                     }
-                    if (lane == i) my_live = live;
                 }
                 if (inside && (!INPLACE || mine || allow[u] != ALL)) store_logits<DT>(out + lane * PT, x[u], v0, q.V);
             }

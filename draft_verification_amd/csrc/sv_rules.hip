@@ -52,18 +52,26 @@ __device__ __forceinline__ void bad_input(int* status)
     if (status) __hip_atomic_fetch_or(status, SV_STATUS_BAD_INPUT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// A value that every lane reads alike and no kernel of the call writes, through
+// the scalar cache.
+template <typename T>
+__device__ __forceinline__ T uniform(const T* p)
+{
+    return *(const __attribute__((address_space(4))) T*)(uintptr_t)p;
+}
+
 // First row and number of rows that the call processes of sequence b; a
 // negative count marks a bad one.
 __device__ __forceinline__ int rows_of(const Rules& q, int b, long long& first)
 {
     if (q.roff) {
-        first = q.roff[b];
-        const long long n = q.roff[b + 1] - first;
+        first = uniform(q.roff + b);
+        const long long n = uniform(q.roff + b + 1) - first;
         return n < 0 || n > q.rows ? -1 : (int)n;
     }
     first = 0;
     if (!q.vlen) return q.rows;
-    const int L = q.vlen[b];
+    const int L = uniform(q.vlen + b);
     if (L < 0) return -1;
     return L < q.row0 ? 0 : (L - q.row0 < q.rows ? L - q.row0 + 1 : q.rows);
 }
@@ -75,9 +83,17 @@ __global__ __launch_bounds__(kThreads) void sv_rules_start_kernel(Rules q)
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (i == 0 && q.status) *q.status = 0;
     if (!q.live || i >= (long long)q.B * q.rows) return;
-    const int b = (int)(i / q.rows), r = (int)(i % q.rows);
-    long long first;
-    q.live[i] = q.masks && r < rows_of(q, b, first) && q.midx[i] != -1 ? 0 : -1;
+    int live = -1;
+    if (q.masks && q.midx[i] != -1) {
+        const int b = (int)(i / q.rows), r = (int)(i % q.rows);
+        if (q.roff) {
+            const long long n = q.roff[b + 1] - q.roff[b];
+            if (n <= q.rows && r < n) live = 0;
+        } else if (!q.vlen || q.row0 + r <= q.vlen[b]) {
+            live = 0;
+        }
+    }
+    q.live[i] = live;
 }
 
 __global__ void sv_status_clear_kernel(int* status) { *status = 0; }
@@ -213,7 +229,7 @@ struct Given {
     template <typename T>
     __device__ __forceinline__ T operator()(const T* p, long long i, T otherwise) const
     {
-        const T v = *(p ? p + i : (const T*)any);
+        const T v = uniform(p ? p + i : (const T*)any);
         return p ? v : otherwise;
     }
 };
@@ -224,8 +240,10 @@ struct Tally {
     int done;     // wavefronts that have added theirs
 };
 
-template <int DT, bool INPLACE>
-__device__ __forceinline__ void process_block(const Rules& q, long long item, Listed<DT>& s, Tally& t)
+// RULES: a history, drafted tokens or biases are given; without them only masks
+// are applied, and neither the lists nor their LDS are there.
+template <int DT, bool INPLACE, bool RULES>
+__device__ __forceinline__ void process_block(const Rules& q, unsigned item, Listed<DT>& s, Tally& t)
 {
     typedef Vec<DT> X;
     typedef typename X::elem elem;
@@ -233,9 +251,8 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     constexpr int PT = X::PT;
     constexpr int SPAN = 64 * PT; // tokens of a wavefront
     constexpr unsigned ALL = (1u << PT) - 1;
-    const int blk = (int)(item % q.nblk);
-    const long long rest = item / q.nblk;
-    const int r0 = (int)(rest % q.nchunk) * q.chunk, b = (int)(rest / q.nchunk);
+    const unsigned rest = __builtin_amdgcn_readfirstlane(item / (unsigned)q.nblk), blk = item - rest * q.nblk;
+    const int b = __builtin_amdgcn_readfirstlane(rest / (unsigned)q.nchunk), r0 = (rest - b * q.nchunk) * q.chunk;
     const int lane = threadIdx.x & 63;
     const int w0 = (blk * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * SPAN; // the wavefront's first token
     const int v0 = w0 + lane * PT;
@@ -250,15 +267,15 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     const Given give;
     long long first;
     const int n = rows_of(q, b, first);
-    const int given_slot = give(q.slots, b, b);
+    const int given_slot = RULES ? give(q.slots, b, b) : -1;
     float rep = give(q.rep, b, 1.0f), freq = give(q.freq, b, 0.0f), pres = give(q.pres, b, 0.0f);
-    int e0 = give(q.boff, b, 0), e1 = give(q.boff, b + 1, 0);
+    int e0 = RULES ? give(q.boff, b, 0) : 0, e1 = RULES ? give(q.boff, b + 1, 0) : 0;
     const int far = min(q.chunk, q.rows - r0); // rows of the chunk, if the sequence has them all
     int my_mask = -1, my_draft = -1, draft0 = -1;
     if (q.masks && lane < far) my_mask = q.midx[(long long)b * q.rows + r0 + lane];
     const int* draft = q.draft + b * q.dstride;
-    if (q.draft && lane + 1 < far) my_draft = draft[q.row0 + r0 + lane]; // between row lane and the next
-    if (q.draft && lane < q.row0 + r0 + far - 1) draft0 = draft[lane];
+    if (RULES && q.draft && lane + 1 < far) my_draft = draft[q.row0 + r0 + lane]; // between row lane and the next
+    if (RULES && q.draft && lane < q.row0 + r0 + far - 1) draft0 = draft[lane];
 
     if (tells && r0 == 0 && n < 0) bad_input(q.status);
     if (r0 >= n) return;
@@ -313,7 +330,7 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fetch_mask(u + kAhead, allow_next[u]);
 
-    const int j0 = q.draft ? q.row0 + r0 : 0, j1 = q.draft ? q.row0 + r1 - 1 : 0;
+    const int j0 = RULES && q.draft ? q.row0 + r0 : 0, j1 = RULES && q.draft ? q.row0 + r1 - 1 : 0;
     auto add_draft = [&](int y) { // counts token w0 + y once more
         if (lane == 0) {
             const int c = s.cnt[y];
@@ -321,7 +338,7 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
         }
     };
     int listed = 0; // tokens that any row of the chunk touches
-    if (slot >= 0 || j1 > 0 || e0 < e1) {
+    if (RULES && (slot >= 0 || j1 > 0 || e0 < e1)) {
         // history
         if (v0 + PT > q.V) mine &= inside ? (1u << (q.V - v0)) - 1 : 0u;
         {
@@ -482,17 +499,17 @@ __device__ __forceinline__ void process_block(const Rules& q, long long item, Li
     }
 }
 
-template <int DT, bool INPLACE>
-__global__ __launch_bounds__(kThreads, 6) void sv_process_kernel(Rules q)
+template <int DT, bool INPLACE, bool RULES>
+__global__ __launch_bounds__(kThreads, RULES ? 6 : 8) void sv_process_kernel(Rules q)
 {
-    __shared__ __align__(16) Listed<DT> lists[kThreads / 64];
+    __shared__ __align__(16) Listed<DT> lists[RULES ? kThreads / 64 : 1];
     __shared__ Tally tally;
     if (threadIdx.x < 64) tally.live[threadIdx.x] = 0;
     if (threadIdx.x == 0) tally.done = 0;
     __syncthreads();
-    const long long items = (long long)q.B * q.nchunk * q.nblk;
-    for (long long i = blockIdx.x; i < items; i += gridDim.x) {
-        process_block<DT, INPLACE>(q, i, lists[threadIdx.x >> 6], tally);
+    const unsigned items = (unsigned)q.B * q.nchunk * q.nblk; // fewer than 2^31: the configuration's limits
+    for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
+        process_block<DT, INPLACE, RULES>(q, i, lists[RULES ? threadIdx.x >> 6 : 0], tally);
         if (gridDim.x < items) __syncthreads(); // the tally is cleared before the next block's counts
     }
 }
@@ -631,7 +648,10 @@ hipError_t launch_process(Rules q, hipStream_t s)
     q.chunk = std::min(64, (q.rows + q.nchunk - 1) / q.nchunk);
     q.nchunk = (q.rows + q.chunk - 1) / q.chunk;
     const long long wgs = std::min(by_seq * q.nchunk, 0xffffffffll / kThreads);
-    return launch_kernel(sv_process_kernel<DT, INPLACE>, dim3((unsigned)wgs), dim3(kThreads), 0, s, nullptr, nullptr, q);
+    const dim3 grid((unsigned)wgs), block(kThreads);
+    return q.counts || q.draft || q.boff
+        ? launch_kernel(sv_process_kernel<DT, INPLACE, true>, grid, block, 0, s, nullptr, nullptr, q)
+        : launch_kernel(sv_process_kernel<DT, INPLACE, false>, grid, block, 0, s, nullptr, nullptr, q);
 }
 
 } // namespace

@@ -119,11 +119,26 @@ struct Vec<SV_BF16> {
         pairs p = __builtin_bit_cast(pairs, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned lo = (unsigned)((int)(bits << (31 - 2 * i)) >> 31), hi = (unsigned)((int)(bits << (30 - 2 * i)) >> 31);
+            const unsigned lo = (unsigned)__builtin_amdgcn_sbfe((int)bits, 2 * i, 1), hi = (unsigned)__builtin_amdgcn_sbfe((int)bits, 2 * i + 1, 1);
             const unsigned keep = (lo & 0xffffu) | (hi & 0xffff0000u);
             p[i] = (p[i] & keep) | (0xff80ff80u & ~keep);
         }
         x = __builtin_bit_cast(raw, p);
+    }
+
+    // Whether a token is infinite or NaN.
+    static __device__ __forceinline__ bool special(const raw& x)
+    {
+        typedef unsigned short two __attribute__((ext_vector_type(2)));
+        typedef unsigned pairs __attribute__((ext_vector_type(4)));
+        const pairs p = __builtin_bit_cast(pairs, x) & 0x7fff7fffu;
+        two m = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned one = p[i];
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(two, one));
+        }
+        return m[0] >= 0x7f80 || m[1] >= 0x7f80;
     }
 };
 
@@ -154,6 +169,13 @@ struct Vec<SV_F32> {
 #pragma unroll
         for (int k = 0; k < PT; ++k) x[k] = bits >> k & 1 ? x[k] : -INFINITY;
     }
+    static __device__ __forceinline__ bool special(const raw& x)
+    {
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < PT; ++k) any |= !(fabsf(x[k]) < INFINITY);
+        return any;
+    }
 };
 
 // A lane's PT bits of a bit row, from token v0 (a multiple of PT).
@@ -164,12 +186,16 @@ __device__ __forceinline__ unsigned bits_at(const unsigned* row, int v0)
     return PT == 8 ? byte : (byte >> (v0 & 4)) & 15u;
 }
 
-// A lane's PT logits; past the row's end they read as -infinity.
-template <int DT>
+// A lane's PT logits; past the row's end they read as -infinity.  Stores are
+// non-temporal, and loads too where the rows are copied (4352 rows of 129280
+// bf16: 450 us, with other loads 465, with neither 474); in place the loaded
+// lines are written in part, and stay for that (1360 masked rows of 50264: 42
+// us, with non-temporal loads 61).
+template <int DT, bool INPLACE>
 __device__ __forceinline__ typename Vec<DT>::raw load_logits(const typename Vec<DT>::elem* p, int v0, int V)
 {
     typedef Vec<DT> X;
-    if (v0 + X::PT <= V) return __builtin_nontemporal_load((const typename X::raw*)p);
+    if (v0 + X::PT <= V) return INPLACE ? *(const typename X::raw*)p : __builtin_nontemporal_load((const typename X::raw*)p);
     typename X::raw x;
 #pragma unroll
     for (int k = 0; k < X::PT; ++k) x[k] = v0 + k < V ? p[k] : X::none();
@@ -211,7 +237,7 @@ __device__ __forceinline__ void wave_sync()
 // time HBM takes: 737 us at B = 256, 17 rows, V = 129280 bf16 where this takes
 // 521.)  The next row adds one drafted token to the counts.  kAhead rows are in
 // flight, and the first are asked for before the rules are read.
-constexpr int kAhead = 4;
+constexpr int kAhead = 2;
 
 template <int DT>
 struct Listed {
@@ -302,7 +328,7 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
     raw x[kAhead];
     unsigned allow[kAhead], allow_next[kAhead];
     auto fetch = [&](int i, raw& xr) {
-        if (r0 + i < r1 && inside) xr = load_logits<DT>(src + i * q.irs, v0, q.V);
+        if (r0 + i < r1 && inside) xr = load_logits<DT, INPLACE>(src + i * q.irs, v0, q.V);
     };
     unsigned mine = 0; // the lane's touched tokens
     if (slot >= 0 && inside) mine = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
@@ -419,7 +445,7 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
         return l + s.bias[y];
     };
     // in place, an unmasked row's touched tokens are changed one by one, and a
-    // masked row's logits are read where they matter
+    // masked row's logits are read and written where they matter
     auto fetch_where = [&](int i, raw& xr, unsigned al) {
         if (!INPLACE) fetch(i, xr);
         else if (r0 + i < r1 && mask_of(i) != -1 && al && (q.live || mine || al != ALL)) fetch(i, xr);
@@ -461,13 +487,23 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
                     wave_sync();
                 }
                 if (masked) {
-                    X::mask(x[u], allow[u]);
-                    if (q.live) { // lanes and tokens past the row's end are -infinity here
-                        int n = 0;
+                    if (!__any(allow[u])) { // a grammar often leaves nothing of a span
 #pragma unroll
-                        for (int k = 0; k < PT; ++k) n += X::get(x[u][k]) > -INFINITY;
-                        n = wave_total(n);
-                        if (lane == i) my_live = n;
+                        for (int k = 0; k < PT; ++k) x[u][k] = X::none();
+                    } else {
+                        // live: the allowed tokens, if none of the row's is infinite or NaN
+                        const bool plain = q.live && !__any(allow[u] && X::special(x[u]));
+                        X::mask(x[u], allow[u]);
+                        if (q.live) {
+                            int n = __popc(allow[u]);
+                            if (!plain || w0 + SPAN > q.V) { // tokens past the row's end are -infinity here
+                                n = 0;
+#pragma unroll
+                                for (int k = 0; k < PT; ++k) n += X::get(x[u][k]) > -INFINITY;
+                            }
+                            n = wave_total(n);
+                            if (lane == i) my_live = n;
+                        }
                     }
                 }
                 if (inside && (!INPLACE || mine || allow[u] != ALL)) store_logits<DT>(out + lane * PT, x[u], v0, q.V);
@@ -500,7 +536,7 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
 }
 
 template <int DT, bool INPLACE, bool RULES>
-__global__ __launch_bounds__(kThreads, RULES ? 6 : 8) void sv_process_kernel(Rules q)
+__global__ __launch_bounds__(kThreads, 6) void sv_process_kernel(Rules q)
 {
     __shared__ __align__(16) Listed<DT> lists[RULES ? kThreads / 64 : 1];
     __shared__ Tally tally;

@@ -97,6 +97,7 @@ __global__ __launch_bounds__(kThreads) void sv_head_pack_kernel(Pack q)
                     word = e;
                 }
             }
+            if (FMT == SV_W4_INT4) word = word << 3 | word >> 29; // pair 0 where widening wants it
             q.packed[i * 4 + w] = word;
         }
         if (FMT == SV_W4_FP4) {
@@ -143,9 +144,10 @@ __device__ __forceinline__ float fp4_scale(unsigned word, int p)
 }
 
 // INT4: code + 16, whose bf16 has the code in the top four bits of its
-// fraction: a shift and one and-or make two of them.  The and-or takes no
-// literal and one scalar operand, so its constants are held in a scalar and a
-// vector register.
+// fraction.  A word holds pair p of its eight codes at bits 3 + 4 p and 19 + 4 p
+// (round the end), so a shift, none for pair 0, and one and-or make two of them.
+// The and-or takes no literal and one scalar operand, so its constants are held
+// in a scalar and a vector register.
 struct Int4Bits {
     unsigned mask, expo;
     __device__ __forceinline__ Int4Bits() : mask(0x00780078u), expo(0x41804180u)
@@ -156,10 +158,10 @@ struct Int4Bits {
     __device__ __forceinline__ bf16x8 widen(unsigned w) const
     {
         union { unsigned u[4]; bf16x8 v; } u;
-        u.u[0] = (w << 3 & mask) | expo;
-        u.u[1] = (w >> 1 & mask) | expo;
-        u.u[2] = (w >> 5 & mask) | expo;
-        u.u[3] = (w >> 9 & mask) | expo;
+        u.u[0] = (w & mask) | expo;
+        u.u[1] = (w >> 4 & mask) | expo;
+        u.u[2] = (w >> 8 & mask) | expo;
+        u.u[3] = ((w >> 12 | w << 20) & mask) | expo;
         return u.v;
     }
 };
@@ -382,7 +384,12 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
     auto load_w = [&](int step, int j) { // past the end: the last step again, not used
         const long long at = min(step, steps - 1);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[j][t] = *(const u32x4*)(wp + at * 4096 + t * 1024 + lane * 16);
+        for (int t = 0; t < 4; ++t) {
+            const u32x4* from = (const u32x4*)(wp + at * 4096 + t * 1024 + lane * 16);
+            // up to 32 rows there is one row block, and the weights are read once
+            // (16 rows at V = 129280, H = 7168: 79 us, with other loads 86)
+            w[j][t] = MT < 4 ? __builtin_nontemporal_load(from) : *from;
+        }
         if constexpr (FMT == SV_W4_FP4) s4[j] = *(const u32x4*)(sp + at * 256 + c * 16);
         else s2[j] = ((const sraw*)(sp + at * (GROUPS * 128)))[lane];
     };
@@ -397,6 +404,7 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
         lds_barrier();
         stage_x(j ^ 1);
         load_x(step + 2);
+        __builtin_amdgcn_sched_barrier(0); // the loads stay ahead of the products
         auto hidden = [&](int mt, int p) { return __builtin_bit_cast(bf16x8, xt[j][mt][x_slot(4 * p + g, c)]); };
         if constexpr (FMT == SV_W4_FP4) {
 #pragma unroll
@@ -429,12 +437,15 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
                     }
 #pragma unroll
                     for (int t = 0; t < 4; ++t) d[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t], b, d[mt][t], 0, 0, 0);
-                    if (p == 3) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) add_scaled(acc[mt][t], d[mt][t], scales[wave][g * 4 + t]);
-                    }
                 }
             }
+            f32x4 s[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) s[t] = scales[wave][g * 4 + t];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) add_scaled(acc[mt][t], d[mt][t], s[t]);
         } else {
             constexpr int P = 4 / GROUPS; // products of a group
 #pragma unroll
@@ -473,6 +484,7 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
             }
         }
         load_w(step + 2, j);
+        __builtin_amdgcn_sched_barrier(0);
     };
 
     load_x(0);

@@ -588,6 +588,19 @@ __device__ __forceinline__ int hist_seq(const Hist& q, int b, long long& first, 
     return bad ? -1 : slot;
 }
 
+// Clears a slot's counts, thread t of `threads` (non-temporal: 256 slots of
+// 129280 in 40 us with the rest of their call, 48 with other stores).
+__device__ __forceinline__ void zero_counts(int* c, int V, int t, int threads)
+{
+    typedef int four __attribute__((ext_vector_type(4), aligned(4)));
+    const four zero = {0, 0, 0, 0};
+    for (int v = t * 4; v < V; v += threads * 4) {
+        if (v + 4 <= V) __builtin_nontemporal_store(zero, (four*)(c + v));
+        else
+            for (int k = v; k < V; ++k) c[k] = 0;
+    }
+}
+
 __global__ __launch_bounds__(kThreads) void sv_history_clear_kernel(Hist q)
 {
     const int b = blockIdx.x / q.per, part = blockIdx.x % q.per;
@@ -595,9 +608,8 @@ __global__ __launch_bounds__(kThreads) void sv_history_clear_kernel(Hist q)
     int n;
     const int slot = hist_seq(q, b, first, n, false);
     if (slot < 0 || !q.reset[b]) return;
-    int* c = q.counts + (long long)slot * q.V;
+    zero_counts(q.counts + (long long)slot * q.V, q.V, part * kThreads + threadIdx.x, q.per * kThreads);
     unsigned* s = q.seen + (long long)slot * q.words;
-    for (int v = part * kThreads + threadIdx.x; v < q.V; v += q.per * kThreads) c[v] = 0;
     for (int v = part * kThreads + threadIdx.x; v < q.words; v += q.per * kThreads) s[v] = 0;
 }
 
@@ -662,6 +674,69 @@ __global__ __launch_bounds__(kBitThreads) void sv_history_bits_kernel(Hist q)
         __syncthreads();
         for (int w = threadIdx.x; w < words; w += kBitThreads)
             if (bits[w]) __hip_atomic_fetch_or(s + w0 + w, bits[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+    }
+}
+
+// A call with resets, in one launch: a workgroup per sequence, which has its
+// slot to itself.  Of several sequences that name one slot the first takes the
+// tokens of all, so that every reset comes before every token and nothing but
+// this workgroup touches the slot: the counts need atomics of its own scope
+// only, the seen bits none.  Bound by the writes of the cleared counts.
+constexpr int kResetBatch = 4096;   // each workgroup looks through the slots of the call
+constexpr int kResetTokens = 32768; // and reads a list alone
+
+__global__ __launch_bounds__(kBitThreads) void sv_history_reset_kernel(Hist q)
+{
+    extern __shared__ unsigned bits[];
+    __shared__ int lower, others, clear;
+    const int b = blockIdx.x;
+    long long first;
+    int n;
+    const int slot = hist_seq(q, b, first, n, threadIdx.x == 0);
+    if (slot < 0) return;
+    if (threadIdx.x == 0) {
+        lower = others = 0;
+        clear = q.reset[b] != 0;
+    }
+    __syncthreads();
+    if (q.slots) // without them, no two sequences share one
+        for (int o = threadIdx.x; o < q.B; o += kBitThreads) {
+            if (o == b || q.slots[o] != slot) continue;
+            long long f;
+            int m;
+            if (hist_seq(q, o, f, m, false) < 0) continue;
+            if (o < b) lower = 1;
+            else others = 1;
+            if (q.reset[o]) clear = 1;
+        }
+    __syncthreads();
+    if (lower) return;
+    const bool share = others, anew = clear;
+    int* c = q.counts + (long long)slot * q.V;
+    unsigned* s = q.seen + (long long)slot * q.words;
+    if (anew) {
+        zero_counts(c, q.V, threadIdx.x, kBitThreads);
+        __syncthreads(); // the zeros are written before a count is added to
+    }
+    for (int w0 = 0; w0 < q.words; w0 += kBitWords) {
+        const int words = min(kBitWords, q.words - w0);
+        for (int w = threadIdx.x; w < words; w += kBitThreads) bits[w] = 0;
+        __syncthreads();
+        for (int o = b; o < (share ? q.B : b + 1); ++o) {
+            if (o > b && (q.slots[o] != slot || hist_seq(q, o, first, n, false) < 0)) continue;
+            for (int i = threadIdx.x; i < n; i += kBitThreads) {
+                const int v = token_at(q, first + i), w = (v >> 5) - w0;
+                if (v < 0 || (unsigned)w >= (unsigned)words) continue;
+                __hip_atomic_fetch_or(bits + w, 1u << (v & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                if (q.kind == SV_HISTORY_OUTPUT) __hip_atomic_fetch_add(c + v, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+        }
+        __syncthreads();
+        for (int w = threadIdx.x; w < words; w += kBitThreads) {
+            if (anew) s[w0 + w] = bits[w];
+            else if (bits[w]) s[w0 + w] |= bits[w];
+        }
         __syncthreads();
     }
 }
@@ -835,8 +910,13 @@ int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, voi
     auto parts = [&](long long items) {
         return (int)std::min(cap, std::max(1ll, (items + kThreads - 1) / kThreads));
     };
+    const size_t lds = sizeof(unsigned) * std::min(kBitWords, q.words);
+    if (e == hipSuccess && q.reset && q.B <= kResetBatch && q.most <= kResetTokens) {
+        e = launch_kernel(sv_history_reset_kernel, dim3((unsigned)q.B), dim3(kBitThreads), (uint32_t)lds, s, nullptr, nullptr, q);
+        return e == hipSuccess ? SV_OK : SV_EDEVICE;
+    }
     if (e == hipSuccess && q.reset) {
-        q.per = std::min(64, parts(q.V));
+        q.per = std::min(64, parts(q.V / 4 + 1));
         e = launch_kernel(sv_history_clear_kernel, dim3((unsigned)((long long)q.B * q.per)), dim3(kThreads), 0, s, nullptr,
                           nullptr, q);
     }
@@ -845,7 +925,6 @@ int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, voi
     // up to 8192 tokens take 8 us with them and 95 without.
     if (e == hipSuccess && q.most >= 512 && (long long)q.B * q.most >= 32768) {
         q.per = (int)std::min(cap / 4, std::min(64ll, (q.most + 8191ll) / 8192));
-        const size_t lds = sizeof(unsigned) * std::min(kBitWords, q.words);
         e = launch_kernel(sv_history_bits_kernel, dim3((unsigned)((long long)q.B * q.per)), dim3(kBitThreads), (uint32_t)lds, s,
                           nullptr, nullptr, q);
     } else if (e == hipSuccess) {

@@ -361,7 +361,7 @@ def test_bad_row_counts_leave_the_rows_alone():
 
 # ---------------------------------------------------------------- history
 
-def _history(B, V, n_slots, sequences, output, *, flat=False, most=None, seed=0, lengths=False, state=None):
+def _history(B, V, n_slots, sequences, output, *, flat=False, most=None, seed=0, lengths=False, state=None, resets=True):
     """One call; sequences: (slot, tokens, reset).  Returns counts, seen (device), status."""
     LB = _lib()
     rng = np.random.default_rng(seed)
@@ -376,7 +376,7 @@ def _history(B, V, n_slots, sequences, output, *, flat=False, most=None, seed=0,
     slots = torch.tensor([s for s, _, _ in sequences], dtype=torch.int32, device=DEV)
     reset = torch.tensor([r for _, _, r in sequences], dtype=torch.int32, device=DEV)
     status = torch.full((1,), -9, dtype=torch.int32, device=DEV)
-    kw = dict(slots=slots, reset=reset, counts=counts, seen=seen, n_slots=n_slots, device_status=status,
+    kw = dict(slots=slots, reset=reset if resets else None, counts=counts, seen=seen, n_slots=n_slots, device_status=status,
               kind=LB.SV_HISTORY_OUTPUT if output else LB.SV_HISTORY_PROMPT, max_tokens=most)
     if flat:
         off = np.concatenate([[0], np.cumsum([len(t) for _, t, _ in sequences])])
@@ -397,6 +397,8 @@ def _history(B, V, n_slots, sequences, output, *, flat=False, most=None, seed=0,
 
 
 @pytest.mark.parametrize("B,V,longest,flat,lengths,output", [
+    (1, 600001, 40000, True, False, True), (2, 600001, 3000, False, False, False), (4100, 65, 3, False, False, True),
+    (9, 5000, 33000, True, False, True), (5, 5000, 33000, True, False, False), (70, 3000, 600, False, True, True),
     (1, 1, 1, False, False, True), (1, 1000, 0, False, False, True), (3, 33, 5, False, True, True), (3, 129280, 700, True, False, True),
     (5, 4097, 3000, True, False, False), (64, 1000, 17, False, False, True), (2, 50257, 20000, False, True, False)])
 def test_history_matches_the_oracle(B, V, longest, flat, lengths, output):
@@ -410,17 +412,21 @@ def test_history_matches_the_oracle(B, V, longest, flat, lengths, output):
         if n > 2 and not lengths:
             t[1] = -1
         seqs.append((int(slots[b]) if b != 2 else -1, t, int(rng.integers(0, 2))))
-    before, counts, seen, status = _history(B, V, B + 4, seqs, output, flat=flat, lengths=lengths, seed=B)
-    want_c, want_s = before[0].copy(), before[1].copy()
-    R.history_update(want_c, want_s, seqs, output)
-    assert status == 0
-    assert np.array_equal(counts, want_c)
-    assert np.array_equal(seen, R.words(want_s))
+    for resets in (True, False):
+        mine = [(s, t, r if resets else 0) for s, t, r in seqs]
+        before, counts, seen, status = _history(B, V, B + 4, mine, output, flat=flat, lengths=lengths, seed=B, resets=resets)
+        want_c, want_s = before[0].copy(), before[1].copy()
+        R.history_update(want_c, want_s, mine, output)
+        assert status == 0
+        assert np.array_equal(counts, want_c)
+        assert np.array_equal(seen, R.words(want_s))
 
 
-def test_two_sequences_of_one_slot_both_count():
-    seqs = [(1, [3, 3, 5], 1), (1, [3, 7], 0), (1, [9], 1)]
-    before, counts, seen, status = _history(3, 100, 2, seqs, True)
+@pytest.mark.parametrize("seqs", [
+    [(1, [3, 3, 5], 1), (1, [3, 7], 0), (1, [9], 1)], [(1, [3, 3, 5], 0), (0, [8], 0), (1, [3, 7], 1)],
+    [(0, [2], 0), (1, [1] * 700, 0), (0, [2] * 40, 0), (1, [], 0)], [(0, [2] * 33000, 0), (0, [4], 1), (1, [5], 0)]])
+def test_two_sequences_of_one_slot_both_count(seqs):
+    before, counts, seen, status = _history(len(seqs), 100, 2, seqs, True)
     want_c, want_s = before[0].copy(), before[1].copy()
     R.history_update(want_c, want_s, seqs, True)
     assert status == 0 and np.array_equal(counts, want_c) and np.array_equal(seen, R.words(want_s))

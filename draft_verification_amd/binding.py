@@ -35,6 +35,7 @@ SV_NOALLOC_SCRATCH_BYTES = 16777216
 SV_HISTORY_PROMPT, SV_HISTORY_OUTPUT = 0, 1
 SV_W4_FP4, SV_W4_INT4 = 0, 1
 SV_MAX_HIDDEN = 65536
+SV_MAX_HISTORY_TOKENS = 1 << 30
 
 
 class Config(ctypes.Structure):

@@ -235,7 +235,7 @@ __device__ __forceinline__ void wave_sync()
 // p-th listed token there.  (Every lane computing its own PT tokens instead
 // costs 20 vector instructions a token, about what the chip can issue in the
 // time HBM takes: 737 us at B = 256, 17 rows, V = 129280 bf16 where this takes
-// 521.)  The next row adds one drafted token to the counts.  kAhead rows are in
+// 455, 5.0 TB/s.)  The next row adds one drafted token to the counts.  kAhead rows are in
 // flight, and the first are asked for before the rules are read.
 constexpr int kAhead = 2;
 
@@ -310,7 +310,7 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
     if (r0 + lane + 1 >= r1) my_draft = -1;
     int slot = q.counts ? given_slot : -1;
     const bool slot_ok = slot >= -1 && slot < q.n_slots;
-    const bool rep_ok = rep > 0.0f && rep < INFINITY, freq_ok = fabsf(freq) < INFINITY, pres_ok = fabsf(pres) < INFINITY;
+    const bool rep_ok = rep >= 0x1p-126f && rep < INFINITY, freq_ok = fabsf(freq) < INFINITY, pres_ok = fabsf(pres) < INFINITY;
     const bool bias_ok = e0 >= 0 && e0 <= e1 && e1 <= q.n_biases;
     if (tells && !((slot_ok || !q.counts) && rep_ok && freq_ok && pres_ok && (bias_ok || !q.boff))) bad_input(q.status);
     if (teller && q.masks && (my_mask < -1 || my_mask >= q.n_masks)) bad_input(q.status);
@@ -437,7 +437,8 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
     const float inv = 1.0f / rep;
     auto apply = [&](float l, int y) { // the rules for token w0 + y
         const int c = s.cnt[y];
-        // l / rep: the product with 1 / rep, corrected by its remainder
+        // l / rep: the product with 1 / rep, corrected by its remainder (a division
+        // in full: 464 us for the 456 of 4352 rows of 129280 bf16)
         const float d = l * inv;
         const float e = fmaf(fmaf(-d, rep, l), inv, d);
         if (c) l = l > 0.0f ? (d < INFINITY ? e : d) : l * rep;
@@ -833,7 +834,7 @@ int spec_verify_process(spec_verify_t* h, const spec_verify_process_args* a, voi
     q.rep = a->repetition;
     q.freq = a->frequency;
     q.pres = a->presence;
-    q.boff = a->n_biases ? a->bias_offsets : nullptr;
+    q.boff = a->bias_offsets;
     q.btok = a->bias_tokens;
     q.bval = a->bias_values;
     q.n_biases = a->n_biases;
@@ -868,6 +869,7 @@ int spec_verify_history_check(const spec_verify_config* cfg, const spec_verify_h
     if (a->B == 0) return SV_OK;
     if (!a->counts || !a->seen || a->n_slots < 1 || (!a->slots && a->n_slots < a->B)) return SV_EINVAL;
     if (a->max_tokens && !a->tokens) return SV_EINVAL;
+    if (a->max_tokens > SV_MAX_HISTORY_TOKENS) return SV_EUNSUPPORTED;
     if (a->token_offsets) {
         if (a->lengths || a->n_tokens < 0) return SV_EINVAL;
     } else if (a->token_stride < a->max_tokens) {

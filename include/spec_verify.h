@@ -358,7 +358,7 @@ int spec_verify_schedule(spec_verify_t* h, const spec_verify_sched_args* a, void
  *   seen_v  bit v of history_seen[slot], or v is one of x_1 .. x_j:
  *   l1  = seen_v ? (l > 0 ? l / repetition : l * repetition) : l
  *   l2  = l1 - (frequency * c_v + presence * [c_v > 0])
- *   l3  = l2 + the biases of v, in the order of the list
+ *   l3  = l2 + the sum of v's biases, taken in the order of the list
  *   out = the row's mask allows v ? l3 : -infinity
  * in fp32, rounded once to the logits' type.  NaN and infinite logits follow
  * these formulas; a token that the mask excludes is -infinity whatever its
@@ -377,8 +377,9 @@ int spec_verify_schedule(spec_verify_t* h, const spec_verify_sched_args* a, void
  * The history of a slot is history_counts int32 [n_slots][V], how often each
  * token was generated, and history_seen uint32 [n_slots][ceil(V/32)], bit v%32
  * of word v/32 set for every token of the prompt or the output.  Both start at
- * zero (or at a reset) and are kept by spec_verify_history.  slots[b] is the
- * slot of sequence b (-1: no history); NULL: slot b.
+ * zero (or at a reset) and are kept by spec_verify_history; a count is not
+ * negative and below 2^31 - 1 - max_draft.  slots[b] is the slot of sequence b
+ * (-1: no history); NULL: slot b.
  *
  * Masks: uint32 [n_masks][mask_stride], bit v%32 of word v/32 set: v allowed;
  * mask_index int32 [B][rows] picks each row's (-1: none; rows of a packed
@@ -392,7 +393,7 @@ int spec_verify_schedule(spec_verify_t* h, const spec_verify_sched_args* a, void
  * history), a drafted id outside [0, V) or a bias id outside [0, V) (ignored),
  * bias_offsets outside [0, n_biases] or descending (no biases), a mask index
  * outside [-1, n_masks) (the row is left without a token), a repetition that
- * is not finite and positive (1) or another penalty that is not finite (0).
+ * is not finite and at least 2^-126 (1) or another penalty that is not finite (0).
  * Deterministic: sums have a fixed order and the only atomics are on integers.
  */
 typedef struct {
@@ -439,15 +440,17 @@ int spec_verify_process(spec_verify_t* h, const spec_verify_process_args* a, voi
  *   SV_HISTORY_PROMPT marks each token as seen,
  *   SV_HISTORY_OUTPUT marks it and adds 1 to its count.
  * Two sequences may name one slot: it gets the tokens of both.  slots[b] = -1
- * skips a sequence.  Counts wrap past 2^31 - 1.  device_status as above: an id outside [-1, V) (ignored),
+ * skips a sequence.  device_status as above: an id outside [-1, V) (ignored),
  * a slot outside [-1, n_slots), a length outside [0, max_tokens] or offsets
  * outside [0, n_tokens] or descending (the sequence is skipped, its reset too).
+ * Lists longer than SV_MAX_HISTORY_TOKENS are refused (SV_EUNSUPPORTED).
  */
 enum { SV_HISTORY_PROMPT = 0, SV_HISTORY_OUTPUT = 1 };
+#define SV_MAX_HISTORY_TOKENS (1 << 30)
 
 typedef struct {
     int32_t B;                      /* 0 <= B <= max_batch */
-    int32_t max_tokens;             /* >= 0: the most tokens of a sequence */
+    int32_t max_tokens;             /* 0 .. SV_MAX_HISTORY_TOKENS: the most tokens of a sequence */
     const int32_t* tokens;          /* device */
     int64_t token_stride;           /* >= max_tokens (dense) */
     const int64_t* token_offsets;   /* optional device [B+1]: flat tokens */
@@ -487,9 +490,10 @@ int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, voi
  * row of every sequence's block (logits_stride = the batch stride) are written
  * where spec_verify_process and spec_verify_run read them.  Any strides and
  * any alignment of the types; 16-byte aligned hidden rows are fastest.  Hidden
- * states are finite (a row that is not gives NaN or infinities, in that row
- * only).  A row's result does not depend on the other rows' values, and is the
- * same from run to run.
+ * states are finite, with SV_W4_INT4 below 2^100 in absolute value (a row that
+ * is not gives NaN or infinities, in that row only).  A row's result does not
+ * depend on the other rows' values, and is the same from run to run; calls with
+ * other numbers of rows may add its terms in another order.
  */
 enum { SV_W4_FP4 = 0, SV_W4_INT4 = 1 };
 #define SV_MAX_HIDDEN 65536

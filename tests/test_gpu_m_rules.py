@@ -310,6 +310,56 @@ def test_bad_bias_offsets_mean_no_biases():
         assert np.array_equal(got, rows_out(q, t, strides)[0][1], equal_nan=True)
 
 
+def test_offsets_into_no_biases_are_reported():
+    p = build(Case(biases=0, masks=False))
+    for off, status in (([0, 0, 0, 0], 0), ([0, 0, 1, 1], 1), ([0, -1, 0, 0], 1), ([2 ** 31 - 1] * 4, 1)):
+        sv, a, t, strides = call(p, bias_offsets=torch.tensor(off, dtype=torch.int32, device=DEV))
+        untouched = t["out"].float().cpu().numpy().astype(np.float64)
+        sv.process(a)
+        assert int(t["status"]) == status
+        compare(p, t, strides, untouched)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rep", [2.0 ** -126, 1.2e-38, 3e-20, 1.0, 7.7e19, 3.4e38])
+def test_extreme_repetitions(dtype, rep):
+    # values below the types' normal range (2^-126 for both) may be flushed
+    p = build(Case(dtype=dtype, masks=False, biases=0))
+    p["rep"][:] = rep
+    c = p["c"]
+    top = 3.3895313892515355e38 if dtype == "bf16" else 3.4028234663852886e38
+    for b in range(c.B):
+        s = p["slots"][b]
+        for r in range(c.rows):
+            o, _, size = R.process_row(p["l"][b, r].astype(np.float64), p["draft"][b, :r], p["counts"][s] if s >= 0 else None,
+                                       p["seen_flags"][s] if s >= 0 else None, float(p["rep"][b]), float(p["freq"][b]),
+                                       float(p["pres"][b]), [], None)
+            p["out"][b, r] = np.where(np.abs(o) > 4 * top, np.sign(o) * np.inf, o)
+            p["tol"][b, r] = 6 * 2.0 ** -24 * np.minimum(size, 4 * top) + 2.0 ** -126
+            if dtype == "bf16":
+                p["tol"][b, r] += 2.0 ** -8 * np.minimum(np.abs(o), top)
+    sv, a, t, strides = call(p)
+    untouched = t["out"].float().cpu().numpy().astype(np.float64)
+    sv.process(a)
+    assert int(t["status"]) == 0
+    compare(p, t, strides, untouched)
+
+
+@pytest.mark.parametrize("rep", [1e-39, 1e-45, 0.0])
+def test_repetitions_below_the_normal_range_are_bad(rep):
+    p = build(Case())
+
+    def change(t):
+        t["rep"][1] = rep
+    got, _, _, _ = _expect(p, change, 1)
+    q = build(Case())
+    sv, a, t, strides = call(q)
+    t["rep"][1] = 1.0
+    sv.process(a)
+    assert int(t["status"]) == 0
+    assert np.array_equal(got, rows_out(q, t, strides)[0][1], equal_nan=True)
+
+
 def test_bad_mask_index_leaves_no_token():
     p = build(Case())
     for bad in (-2, 4, 1 << 30):

@@ -114,6 +114,12 @@ def test_history_check_rejects(B, kw):
     assert B.history_check(B.Config(*CFG), _history(B, **kw)) == B.SV_EINVAL
 
 
+def test_history_check_refuses_lists_past_the_limit(B):
+    n = B.SV_MAX_HISTORY_TOKENS
+    for most, rc in ((n, B.SV_OK), (n + 1, B.SV_EUNSUPPORTED), (2 ** 31 - 1, B.SV_EUNSUPPORTED)):
+        assert B.history_check(B.Config(*CFG), _history(B, max_tokens=most, token_stride=2 ** 31)) == rc
+
+
 def _head(B, **kw):
     a = dict(rows=72, hidden=256, format=1, group=64, packed=FAKE, hidden_states=FAKE, hidden_stride=256, logits=FAKE,
              logits_stride=1000)

@@ -718,7 +718,8 @@ __global__ __launch_bounds__(kBitThreads) void sv_history_reset_kernel(Hist q)
     unsigned* s = q.seen + (long long)slot * q.words;
     if (anew) {
         zero_counts(c, q.V, threadIdx.x, kBitThreads);
-        __syncthreads(); // the zeros are written before a count is added to
+        __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt 0: the zeros are in the L2, where the counts are added to
+        __syncthreads();
     }
     for (int w0 = 0; w0 < q.words; w0 += kBitWords) {
         const int words = min(kBitWords, q.words - w0);

@@ -592,13 +592,13 @@ __device__ __forceinline__ int hist_seq(const Hist& q, int b, long long& first, 
     return bad ? -1 : slot;
 }
 
-// Clears a slot's counts, thread t of `threads` (non-temporal: 256 slots of
-// 129280 in 40 us with the rest of their call, 48 with other stores).
-__device__ __forceinline__ void zero_counts(int* c, int V, int t, int threads)
+// Clears a slot's counts from v0 to V, thread t of `threads` (non-temporal: 256
+// slots of 129280 in 40 us with the rest of their call, 48 with other stores).
+__device__ __forceinline__ void zero_counts(int* c, int v0, int V, int t, int threads)
 {
     typedef int four __attribute__((ext_vector_type(4), aligned(4)));
     const four zero = {0, 0, 0, 0};
-    for (int v = t * 4; v < V; v += threads * 4) {
+    for (int v = v0 + t * 4; v < V; v += threads * 4) {
         if (v + 4 <= V) __builtin_nontemporal_store(zero, (four*)(c + v));
         else
             for (int k = v; k < V; ++k) c[k] = 0;
@@ -612,7 +612,7 @@ __global__ __launch_bounds__(kThreads) void sv_history_clear_kernel(Hist q)
     int n;
     const int slot = hist_seq(q, b, first, n, false);
     if (slot < 0 || !q.reset[b]) return;
-    zero_counts(q.counts + (long long)slot * q.V, q.V, part * kThreads + threadIdx.x, q.per * kThreads);
+    zero_counts(q.counts + (long long)slot * q.V, 0, q.V, part * kThreads + threadIdx.x, q.per * kThreads);
     unsigned* s = q.seen + (long long)slot * q.words;
     for (int v = part * kThreads + threadIdx.x; v < q.words; v += q.per * kThreads) s[v] = 0;
 }
@@ -682,23 +682,30 @@ __global__ __launch_bounds__(kBitThreads) void sv_history_bits_kernel(Hist q)
     }
 }
 
-// A call with resets, in one launch: a workgroup per sequence, which has its
-// slot to itself.  Of several sequences that name one slot the first takes the
-// tokens of all, so that every reset comes before every token and nothing but
-// this workgroup touches the slot: the counts need atomics of its own scope
-// only, the seen bits none.  Bound by the writes of the cleared counts.
+// A call with resets, in one launch: kResetParts workgroups per sequence, each with a
+// part of the slot's tokens to itself, for which it reads the whole list.  Of
+// several sequences that name one slot the first takes the tokens of all, so
+// that every reset comes before every token and nothing but this workgroup
+// touches the part: the counts need atomics of its own scope only, the seen bits
+// none.  Bound by the writes of the cleared counts.
 constexpr int kResetBatch = 4096;   // each workgroup looks through the slots of the call
 constexpr int kResetTokens = 32768; // and reads a list alone
+// One slot of 129280 and a list of 900 take the kernel 4.8 us in four parts, 8.1
+// in one, 4.2 in sixteen; calls that reset 256 such slots, lists of up to 500,
+// 29.8, 31.1 and 33.9; 1500 slots of 50257, lists of up to 2000, 105, 118 and 204.
+constexpr int kResetParts = 4;
 
 __global__ __launch_bounds__(kBitThreads) void sv_history_reset_kernel(Hist q)
 {
     extern __shared__ unsigned bits[];
     __shared__ int lower, others, clear;
-    const int b = blockIdx.x;
+    const int b = blockIdx.x / q.per, part = blockIdx.x % q.per;
     long long first;
     int n;
-    const int slot = hist_seq(q, b, first, n, threadIdx.x == 0);
-    if (slot < 0) return;
+    const int slot = hist_seq(q, b, first, n, part == 0 && threadIdx.x == 0);
+    const int share_words = (q.words + q.per - 1) / q.per; // of a part
+    const int begin = part * share_words, end = min(q.words, begin + share_words);
+    if (slot < 0 || begin >= end) return;
     if (threadIdx.x == 0) {
         lower = others = 0;
         clear = q.reset[b] != 0;
@@ -720,12 +727,14 @@ __global__ __launch_bounds__(kBitThreads) void sv_history_reset_kernel(Hist q)
     int* c = q.counts + (long long)slot * q.V;
     unsigned* s = q.seen + (long long)slot * q.words;
     if (anew) {
-        zero_counts(c, q.V, threadIdx.x, kBitThreads);
-        __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt 0: the zeros are in the L2, where the counts are added to
-        __syncthreads();
+        zero_counts(c, begin * 32, min(q.V, end * 32), threadIdx.x, kBitThreads);
+        if (q.kind == SV_HISTORY_OUTPUT) {
+            __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt 0: the zeros are in the L2, where the counts are added to
+            __syncthreads();
+        }
     }
-    for (int w0 = 0; w0 < q.words; w0 += kBitWords) {
-        const int words = min(kBitWords, q.words - w0);
+    for (int w0 = begin; w0 < end; w0 += kBitWords) {
+        const int words = min(kBitWords, end - w0);
         for (int w = threadIdx.x; w < words; w += kBitThreads) bits[w] = 0;
         __syncthreads();
         for (int o = b; o < (share ? q.B : b + 1); ++o) {
@@ -918,7 +927,10 @@ int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, voi
     };
     const size_t lds = sizeof(unsigned) * std::min(kBitWords, q.words);
     if (e == hipSuccess && q.reset && q.B <= kResetBatch && q.most <= kResetTokens) {
-        e = launch_kernel(sv_history_reset_kernel, dim3((unsigned)q.B), dim3(kBitThreads), (uint32_t)lds, s, nullptr, nullptr, q);
+        q.per = kResetParts;
+        const size_t part = sizeof(unsigned) * std::min(kBitWords, (q.words + q.per - 1) / q.per);
+        e = launch_kernel(sv_history_reset_kernel, dim3((unsigned)(q.B * q.per)), dim3(kBitThreads), (uint32_t)part,
+                          s, nullptr, nullptr, q);
         return e == hipSuccess ? SV_OK : SV_EDEVICE;
     }
     if (e == hipSuccess && q.reset) {

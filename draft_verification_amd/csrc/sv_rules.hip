@@ -43,8 +43,8 @@ struct Rules {
     const int* midx;
     int* live;
     int* status;
-    int nblk;          // token blocks of a row
-    int chunk, nchunk; // rows of a workgroup, chunks of a sequence
+    int b0;    // first sequence of the launch
+    int chunk; // rows of a workgroup
 };
 
 __device__ __forceinline__ void bad_input(int* status)
@@ -269,7 +269,7 @@ struct Tally {
 // RULES: a history, drafted tokens or biases are given; without them only masks
 // are applied, and neither the lists nor their LDS are there.
 template <int DT, bool INPLACE, bool RULES>
-__device__ __forceinline__ void process_block(const Rules& q, unsigned item, Listed<DT>& s, Tally& t)
+__device__ __forceinline__ void process_block(const Rules& q, Listed<DT>& s, Tally& t)
 {
     typedef Vec<DT> X;
     typedef typename X::elem elem;
@@ -277,8 +277,7 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
     constexpr int PT = X::PT;
     constexpr int SPAN = 64 * PT; // tokens of a wavefront
     constexpr unsigned ALL = (1u << PT) - 1;
-    const unsigned rest = __builtin_amdgcn_readfirstlane(item / (unsigned)q.nblk), blk = item - rest * q.nblk;
-    const int b = __builtin_amdgcn_readfirstlane(rest / (unsigned)q.nchunk), r0 = (rest - b * q.nchunk) * q.chunk;
+    const int blk = blockIdx.x, r0 = blockIdx.y * q.chunk, b = q.b0 + blockIdx.z;
     const int lane = threadIdx.x & 63;
     const int w0 = (blk * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * SPAN; // the wavefront's first token
     const int v0 = w0 + lane * PT;
@@ -294,7 +293,8 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
     long long first;
     const int n = rows_of(q, b, first);
     const int given_slot = RULES ? give(q.slots, b, b) : -1;
-    float rep = give(q.rep, b, 1.0f), freq = give(q.freq, b, 0.0f), pres = give(q.pres, b, 0.0f);
+    float rep = 1.0f, freq = 0.0f, pres = 0.0f; // without history or drafted tokens only looked at for their range
+    if (RULES || teller) rep = give(q.rep, b, 1.0f), freq = give(q.freq, b, 0.0f), pres = give(q.pres, b, 0.0f);
     int e0 = RULES ? give(q.boff, b, 0) : 0, e1 = RULES ? give(q.boff, b + 1, 0) : 0;
     const int far = min(q.chunk, q.rows - r0); // rows of the chunk, if the sequence has them all
     int my_mask = -1, my_draft = -1, draft0 = -1;
@@ -530,15 +530,16 @@ __device__ __forceinline__ void process_block(const Rules& q, unsigned item, Lis
             const int live = t.live[lane];
             if (live)
                 __hip_atomic_fetch_add(q.live + (long long)b * q.rows + r0 + lane, live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            t.live[lane] = 0;
-            if (lane == 0) t.done = 0;
         }
     }
 }
 
-// Seven wavefronts to a SIMD, as the registers allow: 1605 MB of fp32 rows of
-// about 5 to a sequence take 311 us, with six 335, with eight 294; but 4352 fp32
-// rows, 17 to a sequence, 805, 787 and 838, and bf16 rows 455, 458 and 455.
+// Eight wavefronts to a SIMD (six with bf16's lists, whose LDS allows no more):
+// 1605 MB of fp32 rows, up to 5 to a sequence, take 298 us, with six 335; 4352
+// fp32 rows, 17 to a sequence, 815 and 787.  (Asked for as seven: for eight, scalar
+// registers spill, 308 us.)  One block to a workgroup: a loop over
+// blocks keeps so much in scalar registers that they spill (the masks of 500
+// rows of 50257 took 19.9 us with it, 17.9 without).
 template <int DT, bool INPLACE, bool RULES>
 __global__ __launch_bounds__(kThreads, 7) void sv_process_kernel(Rules q)
 {
@@ -547,11 +548,7 @@ __global__ __launch_bounds__(kThreads, 7) void sv_process_kernel(Rules q)
     if (threadIdx.x < 64) tally.live[threadIdx.x] = 0;
     if (threadIdx.x == 0) tally.done = 0;
     __syncthreads();
-    const unsigned items = (unsigned)q.B * q.nchunk * q.nblk; // fewer than 2^31: the configuration's limits
-    for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
-        process_block<DT, INPLACE, RULES>(q, i, lists[RULES ? threadIdx.x >> 6 : 0], tally);
-        if (gridDim.x < items) __syncthreads(); // the tally is cleared before the next block's counts
-    }
+    process_block<DT, INPLACE, RULES>(q, lists[RULES ? threadIdx.x >> 6 : 0], tally);
 }
 
 // ---------------------------------------------------------------- history
@@ -762,21 +759,25 @@ int words_of(int V) { return (V + 31) / 32; }
 template <int DT, bool INPLACE>
 hipError_t launch_process(Rules q, hipStream_t s)
 {
-    const int span = kThreads * Vec<DT>::PT;
-    q.nblk = (q.V + span - 1) / span;
+    const int span = kThreads * Vec<DT>::PT, nblk = (q.V + span - 1) / span;
     // A workgroup takes all rows of its sequence, so that the rules are read once,
     // unless that leaves fewer workgroups than fill the chip (8 to each of 256
     // compute units): then as many chunks of the rows as do.  A chunk has at most
     // 64 rows, one to a lane.
-    const long long by_seq = (long long)q.B * q.nblk;
-    q.nchunk = (int)std::min((long long)q.rows, (2048 + by_seq - 1) / by_seq);
-    q.chunk = std::min(64, (q.rows + q.nchunk - 1) / q.nchunk);
-    q.nchunk = (q.rows + q.chunk - 1) / q.chunk;
-    const long long wgs = std::min(by_seq * q.nchunk, 0xffffffffll / kThreads);
-    const dim3 grid((unsigned)wgs), block(kThreads);
-    return q.counts || q.draft || q.boff
-        ? launch_kernel(sv_process_kernel<DT, INPLACE, true>, grid, block, 0, s, nullptr, nullptr, q)
-        : launch_kernel(sv_process_kernel<DT, INPLACE, false>, grid, block, 0, s, nullptr, nullptr, q);
+    const long long by_seq = (long long)q.B * nblk;
+    int nchunk = (int)std::min((long long)q.rows, (2048 + by_seq - 1) / by_seq);
+    q.chunk = std::min(64, (q.rows + nchunk - 1) / nchunk);
+    nchunk = (q.rows + q.chunk - 1) / q.chunk;
+    // launches within 2^32 work-items and 65535 workgroups along z
+    const int most = (int)std::min(65535ll, 0xffffffffll / kThreads / ((long long)nblk * nchunk));
+    for (q.b0 = 0; q.b0 < q.B; q.b0 += most) {
+        const dim3 grid(nblk, nchunk, std::min(most, q.B - q.b0)), block(kThreads);
+        const hipError_t e = q.counts || q.draft || q.boff
+            ? launch_kernel(sv_process_kernel<DT, INPLACE, true>, grid, block, 0, s, nullptr, nullptr, q)
+            : launch_kernel(sv_process_kernel<DT, INPLACE, false>, grid, block, 0, s, nullptr, nullptr, q);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 } // namespace
@@ -857,7 +858,7 @@ int spec_verify_process(spec_verify_t* h, const spec_verify_process_args* a, voi
     q.midx = a->mask_index;
     q.live = a->live_tokens;
     q.status = a->device_status;
-    q.nblk = q.chunk = q.nchunk = 0;
+    q.b0 = q.chunk = 0;
     hipError_t e = hipSuccess;
     if (q.live || q.status) {
         const long long rows = q.live ? (long long)q.B * q.rows : 1;

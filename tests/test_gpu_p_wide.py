@@ -220,6 +220,36 @@ def test_many_rows_of_many_sequences():
     assert torch.equal(alone, out)
 
 
+@pytest.mark.parametrize("inplace", [False, True])
+def test_more_sequences_than_one_launch_takes(inplace):
+    B = _lib()
+    Bn, V = 70001, 40
+    rng = np.random.default_rng(11)
+    l = torch.from_numpy((3 * rng.standard_normal((Bn, V))).astype(np.float32)).to(DEV)
+    seen = rng.random((Bn, V)) < 0.3
+    counts = (seen * rng.integers(0, 4, (Bn, V))).astype(np.int32)
+    allowed = rng.random((Bn, V)) < 0.6
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+    out = l.clone() if inplace else torch.zeros_like(l)
+    src = out if inplace else l
+    i32 = dict(dtype=torch.int32, device=DEV)
+    live, status = torch.zeros((Bn, 1), **i32), torch.full((1,), -9, **i32)
+    f = lambda x: torch.full((Bn,), x, device=DEV)
+    keep = [dev(counts), dev(R.words(seen).view(np.int32)), dev(R.words(allowed).view(np.int32)), torch.arange(Bn, **i32)]
+    sv = B.SpecVerify(Bn, 1, V, B.SV_F32)
+    sv.process(B.make_process_args(
+        Bn, 1, logits_in=src, in_strides=(V, V), logits_out=out, out_strides=(V, V), history_counts=keep[0],
+        history_seen=keep[1], n_slots=Bn, repetition=f(1.25), frequency=f(0.5), presence=f(0.25), masks=keep[2],
+        mask_stride=2, n_masks=Bn, mask_index=keep[3], live_tokens=live, device_status=status))
+    assert int(status) == 0
+    host, got, lv = l.cpu().numpy().astype(np.float64), out.cpu().numpy().astype(np.float64), live.cpu().numpy()
+    for b in [0, 1, 65534, 65535, 65536, 65537, 70000] + rng.integers(0, Bn, 300).tolist():
+        o, n, size = R.process_row(host[b], [], counts[b], seen[b], 1.25, 0.5, 0.25, [], allowed[b])
+        with np.errstate(invalid="ignore"):
+            ok = (got[b] == o) | (np.abs(got[b] - o) <= 8 * 2.0 ** -24 * size)
+        assert ok.all() and lv[b, 0] == n, b
+
+
 def test_two_calls_at_once_on_one_handle():
     B = _lib()
     V, H = 50257, 512

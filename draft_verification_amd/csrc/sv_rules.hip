@@ -685,11 +685,16 @@ __global__ __launch_bounds__(kBitThreads) void sv_history_bits_kernel(Hist q)
 // that every reset comes before every token and nothing but this workgroup
 // touches the part: the counts need atomics of its own scope only, the seen bits
 // none.  Bound by the writes of the cleared counts.
-constexpr int kResetBatch = 4096;   // each workgroup looks through the slots of the call
-constexpr int kResetTokens = 32768; // and reads a list alone
+// It saves a launch, about 2 us (256 sequences, slots of 4000: 10.1 us, as a clear
+// and an addition 13.1; of 129280: 28.9 and 29.9), but its workgroups are large and
+// each looks through the slots of the call (512 sequences, slots of 4000: 15.9 and
+// 12.1; 2048: 52 and 18) and reads a list alone (4 lists of up to 32768: 11.6 and
+// 12.3, of up to 131072: 27 and 12).
+constexpr int kResetBatch = 256;
+constexpr int kResetTokens = 32768;
 // One slot of 129280 and a list of 900 take the kernel 4.8 us in four parts, 8.1
 // in one, 4.2 in sixteen; calls that reset 256 such slots, lists of up to 500,
-// 29.8, 31.1 and 33.9; 1500 slots of 50257, lists of up to 2000, 105, 118 and 204.
+// 29.8, 31.1 and 33.9.
 constexpr int kResetParts = 4;
 
 __global__ __launch_bounds__(kBitThreads) void sv_history_reset_kernel(Hist q)
@@ -762,8 +767,9 @@ hipError_t launch_process(Rules q, hipStream_t s)
     const int span = kThreads * Vec<DT>::PT, nblk = (q.V + span - 1) / span;
     // A workgroup takes all rows of its sequence, so that the rules are read once,
     // unless that leaves fewer workgroups than fill the chip (8 to each of 256
-    // compute units): then as many chunks of the rows as do.  A chunk has at most
-    // 64 rows, one to a lane.
+    // compute units): then as many chunks of the rows as do (4 sequences of 17 rows
+    // of 129280 bf16: 16.3 us, by sequence 33.0, by row 22.0; with 1024 or 4096
+    // workgroups wanted 16.7 and 17.4).  A chunk has at most 64 rows, one to a lane.
     const long long by_seq = (long long)q.B * nblk;
     int nchunk = (int)std::min((long long)q.rows, (2048 + by_seq - 1) / by_seq);
     q.chunk = std::min(64, (q.rows + nchunk - 1) / nchunk);

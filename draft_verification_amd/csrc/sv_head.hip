@@ -457,30 +457,34 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         unsigned word = w[j][t][u * P + p];
-                        asm volatile("" : "+v"(word) : : "memory");
+                        asm volatile("" : "+v"(word));
                         a[p][t] = bits.widen(word);
                     }
                     s[t] = scales[wave][u * 16 + g * 4 + t];
                 }
+                f32x4 d[2][4]; // a tile of rows is multiplied while the one before is scaled
+                auto scale_tile = [&](int mt) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        add_scaled(acc[mt][t], d[mt & 1][t], s[t]);
+                        asm("" : "+v"(acc[mt][t])); // one tile after the other, or their sums pile up and spill
+                    }
+                };
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const f32x4 z4 = offset[j][16 * mt + c];
                     const float z = GROUPS == 4 ? z4[u] : z4[2 * u & 3] + z4[(2 * u + 1) & 3];
-                    f32x4 d[4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) d[t] = f32x4{z, z, z, z};
+                    for (int t = 0; t < 4; ++t) d[mt & 1][t] = f32x4{z, z, z, z};
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         const bf16x8 b = hidden(mt, u * P + p);
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][t], b, d[t], 0, 0, 0);
+                        for (int t = 0; t < 4; ++t) d[mt & 1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][t], b, d[mt & 1][t], 0, 0, 0);
                     }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        add_scaled(acc[mt][t], d[t], s[t]);
-                        asm volatile("" : "+v"(acc[mt][t])); // one tile after the other, or their sums pile up and spill
-                    }
+                    if (mt > 0) scale_tile(mt - 1);
                 }
+                scale_tile(MT - 1);
             }
         }
         load_w(step + 2, j);
@@ -559,16 +563,17 @@ hipError_t launch_head(const Head& q, hipStream_t s)
 {
     // A tile workgroup does the work of four strips for 16 MT rows but takes the
     // same time however few of them there are (measured: about 1 us a step for
-    // FP4, 1.5 to 2.5 for INT4 of group 128 to 32, at MT = 4), while the row
+    // FP4, 1.3 to 1.8 for INT4 of group 128 to 32, at MT = 4), while the row
     // workgroups, 4 MT times as many, do 1050 steps of a strip and 16 rows a us on
     // the whole chip whatever their number.  So the tiles need enough workgroups:
     // 64 rows at V = 8000, H = 4096 FP4 take 32 us as tiles and 19 as rows, at V =
-    // 50257 43 and 100; 64 rows at V = 32000 INT4 of group 32 take 83 and 65.  Up
-    // to 8 rows the weights' bytes bound both, and the rows read them faster (one
-    // row at V = 129280, H = 7168: 76 and 87 us).
+    // 50257 43 and 100; INT4 of group 32 at V = 24000 62 and 50, at V = 41000 71 and
+    // 87; of group 64 at V = 16000 46 and 33, at V = 32000 50 and 61.  Up to 8 rows
+    // the weights' bytes bound both, and the rows read them faster (one row at V =
+    // 129280, H = 7168: 76 and 87 us).
     const int mt = q.M <= 16 ? 1 : q.M <= 32 ? 2 : 4;
     const long long tiles = (q.y.strips + 3) / 4 * ((q.M + 16 * mt - 1) / (16 * mt)) * mt;
-    if (q.M <= 8 || tiles < (FMT == SV_W4_FP4 ? 256 : 640)) return launch_rows<FMT, GROUPS, OUT>(q, s);
+    if (q.M <= 8 || tiles < (FMT == SV_W4_FP4 ? 256 : GROUPS == 4 ? 448 : 352)) return launch_rows<FMT, GROUPS, OUT>(q, s);
     if (mt == 1) return launch_tile<FMT, GROUPS, 1, OUT>(q, s);
     if (mt == 2) return launch_tile<FMT, GROUPS, 2, OUT>(q, s);
     return launch_tile<FMT, GROUPS, 4, OUT>(q, s);

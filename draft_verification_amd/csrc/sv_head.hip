@@ -334,8 +334,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void sv_head_rows_kernel(Head q)
 // hidden values are staged one step ahead and asked for one step before that;
 // the weights go straight to the registers of the wavefront that needs them,
 // two steps ahead, and are widened between the products, where the vector unit
-// has time.
-template <int FMT, int GROUPS, int MT, typename OUT>
+// has time.  ONCE: there is one row block, and the weights are read once.
+template <int FMT, int GROUPS, int MT, bool ONCE, typename OUT>
 __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
 {
     typedef unsigned short sraw __attribute__((ext_vector_type(GROUPS)));
@@ -386,9 +386,9 @@ __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const u32x4* from = (const u32x4*)(wp + at * 4096 + t * 1024 + lane * 16);
-            // up to 32 rows there is one row block, and the weights are read once
-            // (16 rows at V = 129280, H = 7168: 79 us, with other loads 86)
-            w[j][t] = MT < 4 ? __builtin_nontemporal_load(from) : *from;
+            // (16 rows at V = 129280, H = 7168: 77 us, with other loads 86; 64 rows at V =
+            // 16000, H = 4096 in four blocks: 19 us, with other loads 16)
+            w[j][t] = ONCE ? __builtin_nontemporal_load(from) : *from;
         }
         if constexpr (FMT == SV_W4_FP4) s4[j] = *(const u32x4*)(sp + at * 256 + c * 16);
         else s2[j] = ((const sraw*)(sp + at * (GROUPS * 128)))[lane];
@@ -554,28 +554,54 @@ template <int FMT, int GROUPS, int MT, typename OUT>
 hipError_t launch_tile(const Head& q, hipStream_t s)
 {
     return in_launches(q, ((q.y.strips + 3) / 4 + 7) / 8 * 8, 256, 16 * MT, sizeof(OUT), [&](const Head& a, dim3 grid, dim3 block) {
-        return launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, OUT>, grid, block, 0, s, nullptr, nullptr, a);
+        if (MT < 4 && a.nblock == 1)
+            return launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, (MT < 4), OUT>, grid, block, 0, s, nullptr, nullptr, a);
+        return launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, false, OUT>, grid, block, 0, s, nullptr, nullptr, a);
     });
 }
+
+// Time of a step of the tiles of 16 MT rows, in us, with up to one workgroup to
+// each of the 256 compute units and with two (measured at H = 4096, V = 16000 and
+// 32000, 64 MT rows).
+template <int FMT, int GROUPS>
+constexpr float kTileStep[3][2] = {{0.62f, 0.97f}, {0.88f, 1.34f}, {1.24f, 2.12f}}; // FP4
+template <>
+constexpr float kTileStep<SV_W4_INT4, 4>[3][2] = {{1.13f, 1.62f}, {1.68f, 2.20f}, {2.20f, 3.20f}};
+template <>
+constexpr float kTileStep<SV_W4_INT4, 2>[3][2] = {{0.89f, 1.28f}, {1.28f, 1.80f}, {1.75f, 2.66f}};
+template <>
+constexpr float kTileStep<SV_W4_INT4, 1>[3][2] = {{0.90f, 1.27f}, {1.15f, 1.63f}, {1.66f, 2.41f}};
 
 template <int FMT, int GROUPS, typename OUT>
 hipError_t launch_head(const Head& q, hipStream_t s)
 {
     // A tile workgroup does the work of four strips for 16 MT rows but takes the
-    // same time however few of them there are (measured: about 1 us a step for
-    // FP4, 1.3 to 1.8 for INT4 of group 128 to 32, at MT = 4), while the row
-    // workgroups, 4 MT times as many, do 1050 steps of a strip and 16 rows a us on
-    // the whole chip whatever their number.  So the tiles need enough workgroups:
-    // 64 rows at V = 8000, H = 4096 FP4 take 32 us as tiles and 19 as rows, at V =
-    // 50257 43 and 100; INT4 of group 32 at V = 24000 62 and 50, at V = 41000 71 and
-    // 87; of group 64 at V = 16000 46 and 33, at V = 32000 50 and 61.  Up to 8 rows
-    // the weights' bytes bound both, and the rows read them faster (one row at V =
-    // 129280, H = 7168: 76 and 87 us).
-    const int mt = q.M <= 16 ? 1 : q.M <= 32 ? 2 : 4;
-    const long long tiles = (q.y.strips + 3) / 4 * ((q.M + 16 * mt - 1) / (16 * mt)) * mt;
-    if (q.M <= 8 || tiles < (FMT == SV_W4_FP4 ? 256 : GROUPS == 4 ? 448 : 352)) return launch_rows<FMT, GROUPS, OUT>(q, s);
-    if (mt == 1) return launch_tile<FMT, GROUPS, 1, OUT>(q, s);
-    if (mt == 2) return launch_tile<FMT, GROUPS, 2, OUT>(q, s);
+    // same time however few of them there are, while the row workgroups, 4 MT times
+    // as many, do 1050 steps of a strip and 16 rows a us on the whole chip whatever
+    // their number.  So what is quickest depends on how many tiles there are, and the
+    // times above say it.  us as rows and as tiles of 16, 32 and 64, H = 4096:
+    //   FP4   16 rows of V = 16000   10   19   24   30
+    //         100 of 8000            30   19   25   31
+    //         256 of 16000          124   53   44   41
+    //         256 of 32000          241  104   76   68
+    //   INT4  64 of 8000, group 64   20   27   35   46
+    //         100 of 16000           52   41   41   49
+    //         256 of 32000          242  129  105   85
+    // Up to 8 rows the weights' bytes bound both, and the rows read them faster (one
+    // row at V = 129280, H = 7168: 72 and 78 us).
+    if (q.M <= 8) return launch_rows<FMT, GROUPS, OUT>(q, s);
+    float least = (float)q.y.strips * ((q.M + 15) / 16) / 1050.0f;
+    int best = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int rows = 16 << i;
+        const long long n = (q.y.strips + 3) / 4 * ((q.M + rows - 1) / rows);
+        const float one = kTileStep<FMT, GROUPS>[i][0], two = kTileStep<FMT, GROUPS>[i][1];
+        const float t = n <= 256 ? one : n <= 512 ? two : two * ((float)n / 512.0f) + one / 2;
+        if (t < least) least = t, best = rows;
+    }
+    if (best == 0) return launch_rows<FMT, GROUPS, OUT>(q, s);
+    if (best == 16) return launch_tile<FMT, GROUPS, 1, OUT>(q, s);
+    if (best == 32) return launch_tile<FMT, GROUPS, 2, OUT>(q, s);
     return launch_tile<FMT, GROUPS, 4, OUT>(q, s);
 }
 

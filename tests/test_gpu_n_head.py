@@ -126,6 +126,23 @@ def test_head_matches_the_product(M, V, H, fmt, group, dtype, pad):
     _check(wt, x, got, dtype)
 
 
+# several blocks of rows in the tiles of 16, 32 and 64 rows, the last of them in part
+BLOCKS = [(100, 8000, 160, "fp4", 32, "f32"), (100, 16001, 288, "fp4", 32, "bf16"), (250, 32010, 160, "fp4", 32, "f32"),
+          (70, 66001, 96, "fp4", 32, "bf16"), (500, 2001, 192, "fp4", 32, "f32"),
+          (100, 16003, 160, "int4", 32, "f32"), (250, 32010, 96, "int4", 32, "bf16"), (70, 66001, 128, "int4", 32, "f32"),
+          (100, 12001, 192, "int4", 64, "bf16"), (250, 32010, 128, "int4", 64, "f32"), (75, 40001, 320, "int4", 64, "f32"),
+          (100, 12001, 256, "int4", 128, "f32"), (250, 32010, 128, "int4", 128, "bf16"), (90, 24001, 384, "int4", 128, "f32")]
+
+
+@pytest.mark.parametrize("M,V,H,fmt,group,dtype", BLOCKS)
+def test_several_blocks_of_rows(M, V, H, fmt, group, dtype):
+    print(f"[case] head M={M} V={V} H={H} {fmt} {group} {dtype}", flush=True)
+    wt = Weights(V, H, fmt, group, seed=M + V)
+    x = _x(np.random.default_rng(M), M, H)
+    got, _ = _run(wt, x, dtype)
+    _check(wt, x, got, dtype)
+
+
 @pytest.mark.parametrize("fmt", ["fp4", "int4"])
 def test_every_code_and_scale_is_decoded(fmt):
     # one hidden value at a time picks one weight: the logits are the weights

@@ -564,13 +564,13 @@ hipError_t launch_tile(const Head& q, hipStream_t s)
 // each of the 256 compute units and with two (measured at H = 4096, V = 16000 and
 // 32000, 64 MT rows).
 template <int FMT, int GROUPS>
-constexpr float kTileStep[3][2] = {{0.62f, 0.97f}, {0.88f, 1.34f}, {1.24f, 2.12f}}; // FP4
+constexpr float kTileStep[3][2] = {{0.57f, 0.92f}, {0.87f, 1.31f}, {1.25f, 2.08f}}; // FP4
 template <>
-constexpr float kTileStep<SV_W4_INT4, 4>[3][2] = {{1.13f, 1.62f}, {1.68f, 2.20f}, {2.20f, 3.20f}};
+constexpr float kTileStep<SV_W4_INT4, 4>[3][2] = {{1.09f, 1.50f}, {1.56f, 2.14f}, {2.15f, 3.17f}};
 template <>
-constexpr float kTileStep<SV_W4_INT4, 2>[3][2] = {{0.89f, 1.28f}, {1.28f, 1.80f}, {1.75f, 2.66f}};
+constexpr float kTileStep<SV_W4_INT4, 2>[3][2] = {{0.83f, 1.25f}, {1.25f, 1.73f}, {1.74f, 2.66f}};
 template <>
-constexpr float kTileStep<SV_W4_INT4, 1>[3][2] = {{0.90f, 1.27f}, {1.15f, 1.63f}, {1.66f, 2.41f}};
+constexpr float kTileStep<SV_W4_INT4, 1>[3][2] = {{0.84f, 1.24f}, {1.11f, 1.58f}, {1.65f, 2.42f}};
 
 template <int FMT, int GROUPS, typename OUT>
 hipError_t launch_head(const Head& q, hipStream_t s)
@@ -581,12 +581,12 @@ hipError_t launch_head(const Head& q, hipStream_t s)
     // their number.  So what is quickest depends on how many tiles there are, and the
     // times above say it.  us as rows and as tiles of 16, 32 and 64, H = 4096:
     //   FP4   16 rows of V = 16000   10   19   24   30
-    //         100 of 8000            30   19   25   31
-    //         256 of 16000          124   53   44   41
-    //         256 of 32000          241  104   76   68
-    //   INT4  64 of 8000, group 64   20   27   35   46
-    //         100 of 16000           52   41   41   49
-    //         256 of 32000          242  129  105   85
+    //         100 of 8000            30   17   24   31
+    //         128 of 16000           62   27   28   34
+    //         256 of 32000          243  101   73   66
+    //   INT4  100 of 8000, group 64  30   25   33   46
+    //         128 of 16000           61   38   38   50
+    //         256 of 32000          241  134  105   85
     // Up to 8 rows the weights' bytes bound both, and the rows read them faster (one
     // row at V = 129280, H = 7168: 72 and 78 us).
     if (q.M <= 8) return launch_rows<FMT, GROUPS, OUT>(q, s);

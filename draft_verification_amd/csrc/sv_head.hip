@@ -334,7 +334,10 @@ __global__ __launch_bounds__(64 * kRowWaves) void sv_head_rows_kernel(Head q)
 // hidden values are staged one step ahead and asked for one step before that;
 // the weights go straight to the registers of the wavefront that needs them,
 // two steps ahead, and are widened between the products, where the vector unit
-// has time.  ONCE: there is one row block, and the weights are read once.
+// has time.  ONCE: there is one row block, and the weights are read once.  Bound by
+// the matrix rate (559 rows, V = 129280, H = 4096: FP4 493 us, 1200 TFLOP/s), for
+// INT4 by that and the vector instructions that widen and scale (group 128 578 us,
+// 64 638, 32 742), and with few rows by the weights' HBM bytes (64 rows FP4 73 us).
 template <int FMT, int GROUPS, int MT, bool ONCE, typename OUT>
 __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
 {

@@ -235,8 +235,8 @@ __device__ __forceinline__ void wave_sync()
 // p-th listed token there.  (Every lane computing its own PT tokens instead
 // costs 20 vector instructions a token, about what the chip can issue in the
 // time HBM takes: 737 us at B = 256, 17 rows, V = 129280 bf16 where this takes
-// 455, 5.0 TB/s.)  The next row adds one drafted token to the counts.  kAhead rows are in
-// flight, and the first are asked for before the rules are read.
+// 450, 5.0 TB/s.)  The next row adds one drafted token to the counts.  kAhead
+// rows are in flight, and the first are asked for before the rules are read.
 constexpr int kAhead = 2;
 
 template <int DT>

@@ -334,7 +334,7 @@ __device__ __forceinline__ void process_block(const Rules& q, Listed<DT>& s, Tal
     if (slot >= 0 && inside) mine = bits_at<PT>(q.seen + (long long)slot * q.words, v0);
     int bias_tok = -1;
     float bias_val = 0.0f;
-    if (e0 + lane < e1) {
+    if (lane < e1 - e0) { // (e0 + lane may be past 2^31 - 1)
         bias_tok = q.btok[e0 + lane];
         bias_val = q.bval[e0 + lane];
     }
@@ -403,12 +403,12 @@ __device__ __forceinline__ void process_block(const Rules& q, Listed<DT>& s, Tal
             }
         }
         // biases, likewise, added in the list's order
-        for (int i0 = e0; i0 < e1; i0 += 64) {
-            const int x = bias_tok, left = e1 - i0;
+        for (int left = e1 - e0; left > 0; left -= 64) {
+            const int x = bias_tok;
             const float val = bias_val;
-            if (i0 + 64 + lane < e1) {
-                bias_tok = q.btok[i0 + 64 + lane];
-                bias_val = q.bval[i0 + 64 + lane];
+            if (lane < left - 64) {
+                bias_tok = q.btok[e1 - left + 64 + lane];
+                bias_val = q.bval[e1 - left + 64 + lane];
             }
             const bool fine = (unsigned)x < (unsigned)q.V;
             if (teller && lane < left && !fine) bad_input(q.status);

@@ -66,8 +66,8 @@ __device__ __forceinline__ int rows_of(const Rules& q, int b, long long& first)
 {
     if (q.roff) {
         first = uniform(q.roff + b);
-        const long long n = uniform(q.roff + b + 1) - first;
-        return n < 0 || n > q.rows ? -1 : (int)n;
+        const long long end = uniform(q.roff + b + 1);
+        return first < 0 || end < first || end - first > q.rows ? -1 : (int)(end - first);
     }
     first = 0;
     if (!q.vlen) return q.rows;
@@ -87,8 +87,8 @@ __global__ __launch_bounds__(kThreads) void sv_rules_start_kernel(Rules q)
     if (q.masks && q.midx[i] != -1) {
         const int b = (int)(i / q.rows), r = (int)(i % q.rows);
         if (q.roff) {
-            const long long n = q.roff[b + 1] - q.roff[b];
-            if (n <= q.rows && r < n) live = 0;
+            const long long first = q.roff[b], end = q.roff[b + 1];
+            if (first >= 0 && end >= first && end - first <= q.rows && r < end - first) live = 0;
         } else if (!q.vlen || q.row0 + r <= q.vlen[b]) {
             live = 0;
         }

@@ -388,8 +388,9 @@ int spec_verify_schedule(spec_verify_t* h, const spec_verify_sched_args* a, void
  * Outputs: logits_out; optional live_tokens int32 [B][rows], for a processed
  * row with a mask the number of tokens above -infinity, -1 for other rows;
  * optional device_status int32 [1], 0 or SV_STATUS_BAD_INPUT if a device value
- * was out of range: a row count outside [0, rows] or a negative verify length
- * (none of the sequence's rows is processed), a slot outside [-1, n_slots) (no
+ * was out of range: a row count outside [0, rows], a negative row offset or a
+ * negative verify length (none of the sequence's rows is processed; where the
+ * packed rows end is not known to the call), a slot outside [-1, n_slots) (no
  * history), a drafted id outside [0, V) or a bias id outside [0, V) (ignored),
  * bias_offsets outside [0, n_biases] or descending (no biases), a mask index
  * outside [-1, n_masks) (the row is left without a token), a repetition that

@@ -50,3 +50,29 @@ def test_bias_lists_up_to_the_last_32_bit_index(inplace):
         named = np.zeros(V, bool)
         named[ids[at]] = True
         assert np.array_equal(got[b][~named], l[b][~named])
+
+
+@pytest.mark.parametrize("off", [[-2, 0, 2, 3], [-1, 1, 3, 4], [-3, -1, 2, 3], [-2 ** 63, 0, 1, 3], [0, 2, -1, 1]])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_rows_before_the_first_are_left_alone(off, inplace):
+    # the buffers go on before the call's first row, so that what lies there can be looked at
+    B = _lib()
+    V, before, rows = 600, 4, 3
+    src = torch.full((before + 6, V), 2.0, device=DEV)
+    out = src if inplace else torch.full((before + 6, V), 55.0, device=DEV)
+    was = out.clone()
+    live, status = torch.full((3, rows), -9, dtype=torch.int32, device=DEV), torch.full((1,), -9, dtype=torch.int32, device=DEV)
+    mask = torch.full((1, (V + 31) // 32), 0x0f0f0f0f, dtype=torch.int32, device=DEV)
+    B.SpecVerify(3, rows, V, B.SV_F32).process(B.make_process_args(
+        3, rows, logits_in=src[before:], in_strides=(0, V), logits_out=out[before:], out_strides=(0, V),
+        row_offsets=torch.tensor(off, dtype=torch.int64, device=DEV), masks=mask, mask_stride=mask.shape[1], n_masks=1,
+        mask_index=torch.zeros((3, rows), dtype=torch.int32, device=DEV), live_tokens=live, device_status=status))
+    assert int(status) == B.SV_STATUS_BAD_INPUT
+    allowed = torch.from_numpy(R.bits(mask[0].cpu().numpy().view(np.uint32), V)).to(DEV)
+    row = torch.where(allowed, 2.0, -float("inf"))
+    for b in range(3):
+        n = off[b + 1] - off[b] if off[b] >= 0 and off[b] <= off[b + 1] <= off[b] + rows else 0
+        assert live[b].tolist() == [int(allowed.sum())] * n + [-1] * (rows - n)
+        for r in range(n):
+            was[before + off[b] + r] = row
+    assert torch.equal(out, was)

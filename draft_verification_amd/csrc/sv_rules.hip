@@ -696,6 +696,7 @@ constexpr int kResetTokens = 32768;
 // in one, 4.2 in sixteen; calls that reset 256 such slots, lists of up to 500,
 // 29.8, 31.1 and 33.9.
 constexpr int kResetParts = 4;
+static_assert((SV_MAX_VOCAB / 32 + kResetParts - 1) / kResetParts <= kBitWords, "a part's bits are gathered in one go");
 
 __global__ __launch_bounds__(kBitThreads) void sv_history_reset_kernel(Hist q)
 {
@@ -735,25 +736,22 @@ __global__ __launch_bounds__(kBitThreads) void sv_history_reset_kernel(Hist q)
             __syncthreads();
         }
     }
-    for (int w0 = begin; w0 < end; w0 += kBitWords) {
-        const int words = min(kBitWords, end - w0);
-        for (int w = threadIdx.x; w < words; w += kBitThreads) bits[w] = 0;
-        __syncthreads();
-        for (int o = b; o < (share ? q.B : b + 1); ++o) {
-            if (o > b && (q.slots[o] != slot || hist_seq(q, o, first, n, false) < 0)) continue;
-            for (int i = threadIdx.x; i < n; i += kBitThreads) {
-                const int v = token_at(q, first + i), w = (v >> 5) - w0;
-                if (v < 0 || (unsigned)w >= (unsigned)words) continue;
-                __hip_atomic_fetch_or(bits + w, 1u << (v & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                if (q.kind == SV_HISTORY_OUTPUT) __hip_atomic_fetch_add(c + v, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-            }
+    const int words = end - begin;
+    for (int w = threadIdx.x; w < words; w += kBitThreads) bits[w] = 0;
+    __syncthreads();
+    for (int o = b; o < (share ? q.B : b + 1); ++o) {
+        if (o > b && (q.slots[o] != slot || hist_seq(q, o, first, n, false) < 0)) continue;
+        for (int i = threadIdx.x; i < n; i += kBitThreads) {
+            const int v = token_at(q, first + i), w = (v >> 5) - begin;
+            if (v < 0 || (unsigned)w >= (unsigned)words) continue;
+            __hip_atomic_fetch_or(bits + w, 1u << (v & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            if (q.kind == SV_HISTORY_OUTPUT) __hip_atomic_fetch_add(c + v, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
-        __syncthreads();
-        for (int w = threadIdx.x; w < words; w += kBitThreads) {
-            if (anew) s[w0 + w] = bits[w];
-            else if (bits[w]) s[w0 + w] |= bits[w];
-        }
-        __syncthreads();
+    }
+    __syncthreads();
+    for (int w = threadIdx.x; w < words; w += kBitThreads) {
+        if (anew) s[begin + w] = bits[w];
+        else if (bits[w]) s[begin + w] |= bits[w];
     }
 }
 
@@ -935,7 +933,7 @@ int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, voi
     const size_t lds = sizeof(unsigned) * std::min(kBitWords, q.words);
     if (e == hipSuccess && q.reset && q.B <= kResetBatch && q.most <= kResetTokens) {
         q.per = kResetParts;
-        const size_t part = sizeof(unsigned) * std::min(kBitWords, (q.words + q.per - 1) / q.per);
+        const size_t part = sizeof(unsigned) * ((q.words + q.per - 1) / q.per);
         e = launch_kernel(sv_history_reset_kernel, dim3((unsigned)(q.B * q.per)), dim3(kBitThreads), (uint32_t)part,
                           s, nullptr, nullptr, q);
         return e == hipSuccess ? SV_OK : SV_EDEVICE;

@@ -76,3 +76,29 @@ def test_rows_before_the_first_are_left_alone(off, inplace):
         for r in range(n):
             was[before + off[b] + r] = row
     assert torch.equal(out, was)
+
+
+@pytest.mark.parametrize("V", [2 ** 20, 2 ** 20 - 37, 131, 33])
+@pytest.mark.parametrize("output", [True, False])
+def test_reset_of_a_shared_slot_over_the_whole_vocabulary(V, output):
+    # sequences 0, 2 and 3 share a slot, one of them resets it; 1 and 4 have theirs, reset and not
+    B = _lib()
+    rng = np.random.default_rng(V)
+    seqs = [(2, 700, 0), (0, 300, 1), (2, 0, 1), (2, 2000, 0), (1, 500, 0)]
+    tokens = np.full((5, 2000), -1, np.int32)
+    for b, (_, n, _) in enumerate(seqs):
+        tokens[b, :n] = rng.integers(0, V, n)
+        tokens[b, :min(n, 4)] = [0, V - 1, V // 2, 31][:min(n, 4)]
+    counts = rng.integers(0, 5, (4, V)).astype(np.int32)
+    flags = rng.random((4, V)) < 0.1
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    dc, ds, status = up(counts), up(R.words(flags).view(np.int32)), i32([-9])
+    B.SpecVerify(5, 1, V, B.SV_BF16).history(B.make_history_args(
+        5, tokens=up(tokens), token_stride=2000, max_tokens=2000, kind=B.SV_HISTORY_OUTPUT if output else B.SV_HISTORY_PROMPT,
+        slots=i32([s for s, _, _ in seqs]), reset=i32([r for _, _, r in seqs]), counts=dc, seen=ds, n_slots=4,
+        device_status=status))
+    assert int(status) == 0
+    R.history_update(counts, flags, [(s, t[:n], r) for (s, n, r), t in zip(seqs, tokens)], output)
+    assert np.array_equal(dc.cpu().numpy(), counts)
+    assert np.array_equal(ds.cpu().numpy().view(np.uint32), R.words(flags))

@@ -137,7 +137,7 @@ __device__ __forceinline__ bf16x8 widen_fp4(unsigned w, float scale)
 }
 
 // Scale byte p of a word as the exponent of a float, which is all that the
-// conversion reads of it (255: NaN).
+// conversion reads of it (0: 2^-127, 255: NaN).
 __device__ __forceinline__ float fp4_scale(unsigned word, int p)
 {
     return __uint_as_float((p == 3 ? word >> 1 : word << (23 - 8 * p)) & 0x7f800000u);

@@ -102,3 +102,29 @@ def test_reset_of_a_shared_slot_over_the_whole_vocabulary(V, output):
     R.history_update(counts, flags, [(s, t[:n], r) for (s, n, r), t in zip(seqs, tokens)], output)
     assert np.array_equal(dc.cpu().numpy(), counts)
     assert np.array_equal(ds.cpu().numpy().view(np.uint32), R.words(flags))
+
+
+@pytest.mark.parametrize("V,M", [(4096, 8), (65536, 16)])  # split-K workgroups, and tiles
+def test_every_fp4_scale_with_every_code(V, M):
+    # one hidden value at a time picks one weight; where that is in bf16's normal range or zero it is exact
+    B = _lib()
+    H = 32
+    code, s8 = np.arange(V) % 16, (np.arange(V) // 16) % 256
+    w = torch.from_numpy(np.repeat((code | code << 4).astype(np.uint8)[:, None], H // 2, 1)).to(DEV)
+    s = torch.from_numpy(s8.astype(np.uint8)[:, None].copy()).to(DEV)
+    sv = B.SpecVerify(M, 1, V, B.SV_F32)
+    packed = torch.empty(sv.head_packed_bytes(H, B.SV_W4_FP4, 32), dtype=torch.uint8, device=DEV)
+    sv.head_pack(B.make_head_pack_args(hidden=H, format=B.SV_W4_FP4, group=32, weights=w, weight_stride=H // 2, scales=s,
+                                       scale_stride=1, packed=packed))
+    x = torch.eye(H, device=DEV)[:M].to(torch.bfloat16).contiguous()
+    out = torch.empty((M, V), device=DEV)
+    sv.head(B.make_head_args(M, hidden=H, format=B.SV_W4_FP4, group=32, packed=packed, hidden_states=x, hidden_stride=H,
+                             logits=out, logits_stride=V))
+    want = R.FP4[code] * np.ldexp(1.0, s8 - 127)
+    held = (want == 0) | ((np.abs(want) >= 2.0 ** -126) & (np.abs(want) < 2.0 ** 128))
+    held &= s8 < 255
+    assert held[s8 == 0].sum() == 10 * (V // 4096) and held[s8 == 254].sum() == 8 * (V // 4096)
+    got = out.double().cpu().numpy()
+    assert np.isnan(got[:, s8 == 255]).all()
+    bad = np.flatnonzero((got[:, held] != want[held]).any(0))
+    assert bad.size == 0, [(code[held][i], s8[held][i], got[0, held][i], want[held][i]) for i in bad[:8]]

@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "spec_verify.h"
+#include "sv_head_choice.h"
 #include "sv_host.h"
 
 using sv::DeviceGuard;
@@ -18,7 +19,7 @@ using sv::launch_kernel;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStrip = 64;   // vocabulary rows of a strip: 4 matrix-core tiles of 16
+constexpr int kStrip = sv::kHeadStrip; // vocabulary rows of a strip: 4 matrix-core tiles of 16
 constexpr int kStep = 128;   // values of k of a step: 4 products of 32
 
 // Packed weights.  A block of 4 KB is one strip over one step; the blocks of a
@@ -557,55 +558,22 @@ template <int FMT, int GROUPS, int MT, typename OUT>
 hipError_t launch_tile(const Head& q, hipStream_t s)
 {
     return in_launches(q, ((q.y.strips + 3) / 4 + 7) / 8 * 8, 256, 16 * MT, sizeof(OUT), [&](const Head& a, dim3 grid, dim3 block) {
-        if (MT < 4 && a.nblock == 1)
-            return launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, (MT < 4), OUT>, grid, block, 0, s, nullptr, nullptr, a);
+        if (sv::head_tile_once(16 * MT, a.nblock))
+            return launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, sv::head_tile_once(16 * MT, 1), OUT>, grid, block, 0, s, nullptr,
+                                 nullptr, a);
         return launch_kernel(sv_head_tile_kernel<FMT, GROUPS, MT, false, OUT>, grid, block, 0, s, nullptr, nullptr, a);
     });
 }
 
-// Time of a step of the tiles of 16 MT rows, in us, with up to one workgroup to
-// each of the 256 compute units and with two (measured at H = 4096, V = 16000 and
-// 32000, 64 MT rows).
-template <int FMT, int GROUPS>
-constexpr float kTileStep[3][2] = {{0.57f, 0.92f}, {0.87f, 1.31f}, {1.25f, 2.08f}}; // FP4
-template <>
-constexpr float kTileStep<SV_W4_INT4, 4>[3][2] = {{1.09f, 1.50f}, {1.56f, 2.14f}, {2.15f, 3.17f}};
-template <>
-constexpr float kTileStep<SV_W4_INT4, 2>[3][2] = {{0.83f, 1.25f}, {1.25f, 1.73f}, {1.74f, 2.66f}};
-template <>
-constexpr float kTileStep<SV_W4_INT4, 1>[3][2] = {{0.84f, 1.24f}, {1.11f, 1.58f}, {1.65f, 2.42f}};
-
 template <int FMT, int GROUPS, typename OUT>
 hipError_t launch_head(const Head& q, hipStream_t s)
 {
-    // A tile workgroup does the work of four strips for 16 MT rows but takes the
-    // same time however few of them there are, while the row workgroups, 4 MT times
-    // as many, do 1050 steps of a strip and 16 rows a us on the whole chip whatever
-    // their number.  So what is quickest depends on how many tiles there are, and the
-    // times above say it.  us as rows and as tiles of 16, 32 and 64, H = 4096:
-    //   FP4   16 rows of V = 16000   10   19   24   30
-    //         100 of 8000            30   17   24   31
-    //         128 of 16000           62   27   28   34
-    //         256 of 32000          243  101   73   66
-    //   INT4  100 of 8000, group 64  30   25   33   46
-    //         128 of 16000           61   38   38   50
-    //         256 of 32000          241  134  105   85
-    // Up to 8 rows the weights' bytes bound both, and the rows read them faster (one
-    // row at V = 129280, H = 7168: 72 and 78 us).
-    if (q.M <= 8) return launch_rows<FMT, GROUPS, OUT>(q, s);
-    float least = (float)q.y.strips * ((q.M + 15) / 16) / 1050.0f;
-    int best = 0;
-    for (int i = 0; i < 3; ++i) {
-        const int rows = 16 << i;
-        const long long n = (q.y.strips + 3) / 4 * ((q.M + rows - 1) / rows);
-        const float one = kTileStep<FMT, GROUPS>[i][0], two = kTileStep<FMT, GROUPS>[i][1];
-        const float t = n <= 256 ? one : n <= 512 ? two : two * ((float)n / 512.0f) + one / 2;
-        if (t < least) least = t, best = rows;
+    switch (sv::head_tile_rows(q.M, q.y.V, FMT == SV_W4_FP4, kStep / GROUPS)) {
+    case 16: return launch_tile<FMT, GROUPS, 1, OUT>(q, s);
+    case 32: return launch_tile<FMT, GROUPS, 2, OUT>(q, s);
+    case 64: return launch_tile<FMT, GROUPS, 4, OUT>(q, s);
+    default: return launch_rows<FMT, GROUPS, OUT>(q, s);
     }
-    if (best == 0) return launch_rows<FMT, GROUPS, OUT>(q, s);
-    if (best == 16) return launch_tile<FMT, GROUPS, 1, OUT>(q, s);
-    if (best == 32) return launch_tile<FMT, GROUPS, 2, OUT>(q, s);
-    return launch_tile<FMT, GROUPS, 4, OUT>(q, s);
 }
 
 template <typename OUT>

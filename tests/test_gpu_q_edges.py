@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 from oracle import rules as R
+from tests import test_gpu_n_head as N
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,24 @@ def test_every_fp4_scale_with_every_code(V, M):
     assert np.isnan(got[:, s8 == 255]).all()
     bad = np.flatnonzero((got[:, held] != want[held]).any(0))
     assert bad.size == 0, [(code[held][i], s8[held][i], got[0, held][i], want[held][i]) for i in bad[:8]]
+# what test_gpu_n_head.py leaves of the head's kernels in either logits type: split-K workgroups, one block of
+# rows and several in tiles of 16 and 32 rows, tiles of 64, the last block in part, odd and even numbers of steps
+HEADS = [
+    (31, 33001, 288, "fp4", 32, "bf16"), (100, 20001, 160, "fp4", 32, "bf16"),
+    (130, 32010, 352, "int4", 32, "f32"), (12, 164001, 96, "int4", 32, "bf16"), (100, 16003, 160, "int4", 32, "bf16"),
+    (31, 82001, 288, "int4", 32, "bf16"), (70, 32010, 96, "int4", 32, "bf16"),
+    (40, 19001, 320, "int4", 64, "f32"), (31, 82001, 192, "int4", 64, "f32"), (16, 164001, 128, "int4", 64, "bf16"),
+    (130, 32010, 320, "int4", 64, "bf16"),
+    (12, 164001, 384, "int4", 128, "f32"), (100, 8500, 256, "int4", 128, "f32"), (100, 8500, 384, "int4", 128, "f32"),
+    (130, 32010, 128, "int4", 128, "f32"), (12, 7501, 384, "int4", 128, "bf16"), (40, 19001, 256, "int4", 128, "bf16"),
+    (70, 12001, 640, "int4", 128, "bf16"), (31, 40001, 384, "int4", 128, "bf16"), (70, 16003, 128, "int4", 128, "bf16"),
+]
+
+
+@pytest.mark.parametrize("M,V,H,fmt,group,dtype", HEADS)
+def test_head_kernels_in_both_types(M, V, H, fmt, group, dtype):
+    print(f"[case] head M={M} V={V} H={H} {fmt} {group} {dtype}", flush=True)
+    wt = N.Weights(V, H, fmt, group, seed=M + V)
+    x = N._x(np.random.default_rng(M), M, H)
+    got, _ = N._run(wt, x, dtype)
+    N._check(wt, x, got, dtype)

@@ -478,6 +478,11 @@ int spec_verify_history(spec_verify_t* h, const spec_verify_history_args* a, voi
  *               NaN).  Every product of a value and its scale has to be in
  *               bf16's normal range or zero.
  *   SV_W4_INT4  W = (code - 8) * s, one bf16 scale s per 32, 64 or 128 values.
+ * Before its rounding to the logits' type, a result is off by at most
+ * (hidden / 32 + 40) * 2^-23 of sum_k |x[m][k] W[v][k]| with SV_W4_FP4, and of
+ * sum_k |s x[m][k]| (code + 40) with SV_W4_INT4, which sums s (code + 16) x and
+ * takes 24 s sum x off, group by group: rows of codes 8 (a padded vocabulary)
+ * give values of that size and not zeros.
  * Source layout: weights uint8 [V][weight_stride], value k in the low (k even)
  * or high (k odd) half of byte k/2; scales [V][scale_stride] (bytes, or bf16),
  * group g covers k = g*group ..  hidden is a multiple of the group.

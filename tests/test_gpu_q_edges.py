@@ -150,3 +150,31 @@ def test_head_kernels_in_both_types(M, V, H, fmt, group, dtype):
     x = N._x(np.random.default_rng(M), M, H)
     got, _ = N._run(wt, x, dtype)
     N._check(wt, x, got, dtype)
+
+
+@pytest.mark.parametrize("M,V", [(5, 200), (16, 164001), (70, 66001)])  # split-K workgroups, one block in tiles, several
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_error_stays_within_the_stated_bound(M, V, group):
+    # vocabulary rows of codes 8 (weights of zero), of codes 7 and 9, and of any, on hidden values with one sign
+    # and channels 2^10 times the others: where the sum of (code + 16) x and 24 times that of x nearly cancel
+    B = _lib()
+    H = 768
+    rng = np.random.default_rng(group)
+    codes = rng.integers(0, 16, (V, H))
+    codes[0::3] = 8
+    codes[1::3] = 7 + 2 * (codes[1::3] & 1)
+    scale = torch.from_numpy((0.5 + rng.random((V, H // group))).astype(np.float32)).to(torch.bfloat16)
+    x = np.abs(rng.standard_normal((M, H))) + 0.5
+    x[:, ::100] *= 1024
+    x = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)
+    sv = B.SpecVerify(M, 1, V, B.SV_F32)
+    packed = torch.empty(sv.head_packed_bytes(H, B.SV_W4_INT4, group), dtype=torch.uint8, device=DEV)
+    w, s, xd = torch.from_numpy((codes[:, ::2] | codes[:, 1::2] << 4).astype(np.uint8)).to(DEV), scale.to(DEV), x.to(DEV)
+    sv.head_pack(B.make_head_pack_args(hidden=H, format=B.SV_W4_INT4, group=group, weights=w, weight_stride=H // 2, scales=s,
+                                       scale_stride=H // group, packed=packed))
+    out = torch.empty((M, V), device=DEV)
+    sv.head(B.make_head_args(M, hidden=H, format=B.SV_W4_INT4, group=group, packed=packed, hidden_states=xd, hidden_stride=H,
+                             logits=out, logits_stride=V))
+    x64, s64 = x.double().numpy(), np.repeat(scale.double().numpy(), group, 1)
+    off = np.abs(out.double().cpu().numpy() - x64 @ ((codes - 8) * s64).T)
+    assert (off <= (H / 32 + 40) * 2.0 ** -23 * (np.abs(x64) @ ((codes + 40) * s64).T)).all()

@@ -244,8 +244,9 @@ __device__ __forceinline__ float x_offset(u32x4 x)
 // Few rows, or few vocabulary rows: one workgroup of kRowWaves wavefronts per
 // strip and 16 hidden rows.  The wavefronts take the strip's steps in turn, so
 // that the workgroup reads kRowWaves blocks, one after the other in memory, at
-// a time, and join their sums at the end.  Bound by the weights' HBM bytes: 6.8
-// TB/s at one row, V = 129280, H = 7168, FP4 (72 us).  Eight wavefronts with
+// a time, and join their sums at the end.  Bound by the weights' HBM bytes: 6.9
+// TB/s at one row, V = 129280, H = 7168, FP4 (72 us in a long run of calls, 76 in
+// the first hundred after a pause).  Eight wavefronts with
 // one step's loads each beat four with two steps' (the registers of the second
 // leave fewer wavefronts) by 1 to 15%.  INT4's scales go through LDS, since a
 // lane needs those of 16 rows (as loads from memory, they cost the address unit
@@ -336,9 +337,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void sv_head_rows_kernel(Head q)
 // the weights go straight to the registers of the wavefront that needs them,
 // two steps ahead, and are widened between the products, where the vector unit
 // has time.  ONCE: there is one row block, and the weights are read once.  Bound by
-// the matrix rate (559 rows, V = 129280, H = 4096: FP4 493 us, 1200 TFLOP/s), for
-// INT4 by that and the vector instructions that widen and scale (group 128 578 us,
-// 64 638, 32 742), and with few rows by the weights' HBM bytes (64 rows FP4 73 us).
+// the matrix rate (559 rows, V = 129280, H = 4096: FP4 498 us, 1190 TFLOP/s), for
+// INT4 by that and the vector instructions that widen and scale (group 128 587 us,
+// 64 649, 32 765), and with few rows by the weights' HBM bytes (64 rows FP4 73 us).
 template <int FMT, int GROUPS, int MT, bool ONCE, typename OUT>
 __global__ __launch_bounds__(256, 2) void sv_head_tile_kernel(Head q)
 {

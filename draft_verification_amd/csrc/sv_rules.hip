@@ -685,11 +685,15 @@ __global__ __launch_bounds__(kBitThreads) void sv_history_bits_kernel(Hist q)
 // that every reset comes before every token and nothing but this workgroup
 // touches the part: the counts need atomics of its own scope only, the seen bits
 // none.  Bound by the writes of the cleared counts.
-// It saves a launch, about 2 us (256 sequences, slots of 4000: 10.1 us, as a clear
-// and an addition 13.1; of 129280: 28.9 and 29.9), but its workgroups are large and
-// each looks through the slots of the call (512 sequences, slots of 4000: 15.9 and
-// 12.1; 2048: 52 and 18) and reads a list alone (4 lists of up to 32768: 11.6 and
-// 12.3, of up to 131072: 27 and 12).
+// It saves a launch, about 2 us, but its workgroups are large, each looks through
+// the slots of the call, and each reads a list alone.  us in one launch, and as a
+// clear and an addition, lists of 500 ids:
+//   sequences           16         128         256         512
+//   slots of 4000      4.0  6.8   7.4  7.5  11.6 10.7  19.7 17.6   (2048: 52 and 18)
+//   slots of 129280    6.6  6.9  17.5 18.9  31.6 35.4  60.0 67.9
+// and 4 lists of up to 32768 11.6 and 12.3, of up to 131072 27 and 12.  Many
+// sequences on one slot leave its four workgroups all their lists: 256 of 500 ids
+// take 191 us and 30, of 8192 1134 and 100.  The host does not see the slots.
 constexpr int kResetBatch = 256;
 constexpr int kResetTokens = 32768;
 // One slot of 129280 and a list of 900 take the kernel 4.8 us in four parts, 8.1

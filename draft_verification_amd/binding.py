@@ -18,7 +18,7 @@ SV_OK, SV_EINVAL, SV_ENOMEM, SV_EDEVICE, SV_EUNSUPPORTED = 0, -1, -2, -3, -4
 SV_F32, SV_BF16 = 0, 1
 SV_LEN_FIXED, SV_LEN_TAU = 0, 1
 SV_DRAFT_PROBS, SV_DRAFT_ONEHOT = 0, 1
-SV_STATUS_BAD_INPUT, SV_STATUS_INCOMPLETE = 1, 2
+SV_STATUS_BAD_INPUT, SV_STATUS_INCOMPLETE, SV_STATUS_NO_PAGES = 1, 2, 4
 
 EXPORTED = (
     "spec_verify_create", "spec_verify_check", "spec_verify_run", "spec_verify_destroy",
@@ -27,7 +27,9 @@ EXPORTED = (
     "spec_verify_conf_check", "spec_verify_confidence", "spec_verify_run_noalloc",
     "spec_verify_process_check", "spec_verify_process", "spec_verify_history_check", "spec_verify_history",
     "spec_verify_head_packed_bytes", "spec_verify_head_pack_check", "spec_verify_head_pack",
-    "spec_verify_head_check", "spec_verify_head",
+    "spec_verify_head_check", "spec_verify_head", "spec_verify_pages_check", "spec_verify_pages",
+    "spec_verify_pages_copy_check", "spec_verify_pages_copy", "spec_verify_append_check", "spec_verify_append",
+    "spec_verify_attend_workspace_bytes", "spec_verify_attend_check", "spec_verify_attend",
 )
 SV_MAX_CONF_DELAY = 4
 SV_MAX_SCHED_BATCH, SV_MAX_SCHED_CANDIDATES = 4096, 65536
@@ -36,6 +38,10 @@ SV_HISTORY_PROMPT, SV_HISTORY_OUTPUT = 0, 1
 SV_W4_FP4, SV_W4_INT4 = 0, 1
 SV_MAX_HIDDEN = 65536
 SV_MAX_HISTORY_TOKENS = 1 << 30
+SV_PAGES_CLEAR, SV_PAGES_RESERVE, SV_PAGES_COMMIT, SV_PAGES_RELEASE, SV_PAGES_FORK, SV_PAGES_COMPACT = range(6)
+SV_KV_BF16, SV_KV_E4M3 = 0, 1
+SV_MAX_PAGES, SV_MAX_PAGE_SIZE, SV_MAX_CACHE_TOKENS = 1 << 24, 1024, 1 << 30
+SV_MAX_PAGE_BATCH, SV_MAX_PAGE_ROWS, SV_MAX_HEAD_DIM = 4096, 1 << 20, 256
 
 
 class Config(ctypes.Structure):
@@ -122,6 +128,62 @@ class HeadArgs(ctypes.Structure):
     ]
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [
+        ("n_slots", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+        ("page_counts", ctypes.c_void_p), ("page_refs", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+    ]
+
+
+class PagesArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("kind", ctypes.c_int32), ("cache", Cache), ("slots", ctypes.c_void_p),
+        ("from_slots", ctypes.c_void_p), ("rows", ctypes.c_int32), ("last_row", ctypes.c_void_p),
+        ("granted", ctypes.c_void_p), ("copies", ctypes.c_void_p), ("max_copies", ctypes.c_int32),
+        ("device_status", ctypes.c_void_p),
+    ]
+
+
+class PagesCopyArgs(ctypes.Structure):
+    _fields_ = [
+        ("n_copies", ctypes.c_int32), ("copies", ctypes.c_void_p), ("pools", ctypes.c_void_p),
+        ("n_pools", ctypes.c_int32), ("pool_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+        ("page_bytes", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("device_status", ctypes.c_void_p),
+    ]
+
+
+class KV(ctypes.Structure):
+    _fields_ = [
+        ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32),
+        ("keys", ctypes.c_void_p), ("values", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("key_scales", ctypes.c_void_p),
+        ("value_scales", ctypes.c_void_p),
+    ]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("row0", ctypes.c_int32), ("cache", Cache), ("kv", KV),
+        ("slots", ctypes.c_void_p), ("last_row", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+        ("keys", ctypes.c_void_p), ("values", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("device_status", ctypes.c_void_p),
+    ]
+
+
+class AttendArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("row0", ctypes.c_int32), ("cache", Cache), ("kv", KV),
+        ("slots", ctypes.c_void_p), ("last_row", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+        ("heads", ctypes.c_int32), ("queries", ctypes.c_void_p), ("query_batch_stride", ctypes.c_int64),
+        ("query_row_stride", ctypes.c_int64), ("query_head_stride", ctypes.c_int64), ("outputs", ctypes.c_void_p),
+        ("output_batch_stride", ctypes.c_int64), ("output_row_stride", ctypes.c_int64),
+        ("output_head_stride", ctypes.c_int64), ("lse", ctypes.c_void_p), ("scale", ctypes.c_float),
+        ("window", ctypes.c_int32), ("max_len", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64), ("device_status", ctypes.c_void_p),
+    ]
+
+
 class SpecVerifyError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} ({status})")
@@ -169,8 +231,11 @@ def lib() -> ctypes.CDLL:
         L.spec_verify_run_noalloc.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(Args), ctypes.c_void_p]
         L.spec_verify_head_packed_bytes.restype = ctypes.c_int64
         L.spec_verify_head_packed_bytes.argtypes = [ctypes.POINTER(Config)] + [ctypes.c_int32] * 3
+        L.spec_verify_attend_workspace_bytes.restype = ctypes.c_int64
+        L.spec_verify_attend_workspace_bytes.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(AttendArgs)]
         for name, args in (("process", ProcessArgs), ("history", HistoryArgs), ("head_pack", HeadPackArgs),
-                           ("head", HeadArgs)):
+                           ("head", HeadArgs), ("pages", PagesArgs), ("pages_copy", PagesCopyArgs),
+                           ("append", AppendArgs), ("attend", AttendArgs)):
             check_fn, run_fn = getattr(L, f"spec_verify_{name}_check"), getattr(L, f"spec_verify_{name}")
             check_fn.restype = run_fn.restype = ctypes.c_int
             check_fn.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(args)]
@@ -313,6 +378,83 @@ def head_packed_bytes(cfg: Config, hidden: int, format: int, group: int) -> int:
     return n
 
 
+def make_cache(*, n_slots: int, n_pages: int, page_size: int, max_pages: int, page_table, lengths, page_counts=None,
+               page_refs=None, free_pages=None) -> Cache:
+    """Fill a Cache struct (device tensors or addresses)."""
+    return Cache(int(n_slots), int(n_pages), int(page_size), int(max_pages), _addr(page_table), _addr(lengths),
+                 _addr(page_counts), _addr(page_refs), _addr(free_pages))
+
+
+def make_pages_args(B: int, *, kind: int, cache: Cache, slots=None, from_slots=None, rows: int = 0, last_row=None,
+                    granted=None, copies=None, max_copies: int = 0, device_status=None) -> PagesArgs:
+    """Fill a PagesArgs struct (device tensors or addresses)."""
+    return PagesArgs(int(B), int(kind), cache, _addr(slots), _addr(from_slots), int(rows), _addr(last_row),
+                     _addr(granted), _addr(copies), int(max_copies), _addr(device_status))
+
+
+def pages_check(cfg: Config, args: PagesArgs) -> int:
+    """Host-only check of a call on the cache's pages (no device work)."""
+    return int(lib().spec_verify_pages_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def make_pages_copy_args(n_copies: int, *, copies, pools, n_pools: int, pool_stride: int, page_stride: int,
+                         page_bytes: int, n_pages: int, device_status=None) -> PagesCopyArgs:
+    """Fill a PagesCopyArgs struct (device tensors or addresses).  Strides are in bytes."""
+    return PagesCopyArgs(int(n_copies), _addr(copies), _addr(pools), int(n_pools), int(pool_stride), int(page_stride),
+                         int(page_bytes), int(n_pages), _addr(device_status))
+
+
+def pages_copy_check(cfg: Config, args: PagesCopyArgs) -> int:
+    """Host-only check of a copy of pages (no device work)."""
+    return int(lib().spec_verify_pages_copy_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def make_kv(*, kv_heads: int, head_dim: int, type: int, keys, values, strides: Sequence[int], key_scales=None,
+            value_scales=None) -> KV:
+    """Fill a KV struct (device tensors or addresses).  Strides are (page, head, token) in elements."""
+    return KV(int(kv_heads), int(head_dim), int(type), _addr(keys), _addr(values), int(strides[0]), int(strides[1]),
+              int(strides[2]), _addr(key_scales), _addr(value_scales))
+
+
+def make_append_args(B: int, rows: int, *, cache: Cache, kv: KV, keys, values, strides: Sequence[int], row0: int = 0,
+                     slots=None, last_row=None, row_offsets=None, device_status=None) -> AppendArgs:
+    """Fill an AppendArgs struct (device tensors or addresses).  Strides are (batch, row, head) in elements."""
+    return AppendArgs(int(B), int(rows), int(row0), cache, kv, _addr(slots), _addr(last_row), _addr(row_offsets),
+                      _addr(keys), _addr(values), int(strides[0]), int(strides[1]), int(strides[2]),
+                      _addr(device_status))
+
+
+def append_check(cfg: Config, args: AppendArgs) -> int:
+    """Host-only check of an append call (no device work)."""
+    return int(lib().spec_verify_append_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def make_attend_args(B: int, rows: int, *, cache: Cache, kv: KV, heads: int, queries, query_strides: Sequence[int],
+                     outputs, output_strides: Sequence[int], scale: float, row0: int = 0, slots=None, last_row=None,
+                     row_offsets=None, lse=None, window: int = 0, max_len: int = 0, workspace=None,
+                     workspace_bytes: int = 0, device_status=None) -> AttendArgs:
+    """Fill an AttendArgs struct (device tensors or addresses).  Strides are (batch, row, head) in elements.
+    The workspace may be set afterwards, when its size is known."""
+    return AttendArgs(int(B), int(rows), int(row0), cache, kv, _addr(slots), _addr(last_row), _addr(row_offsets),
+                      int(heads), _addr(queries), int(query_strides[0]), int(query_strides[1]), int(query_strides[2]),
+                      _addr(outputs), int(output_strides[0]), int(output_strides[1]), int(output_strides[2]),
+                      _addr(lse), float(scale), int(window), int(max_len), _addr(workspace), int(workspace_bytes),
+                      _addr(device_status))
+
+
+def attend_check(cfg: Config, args: AttendArgs) -> int:
+    """Host-only check of an attend call (no device work)."""
+    return int(lib().spec_verify_attend_check(ctypes.byref(cfg), ctypes.byref(args)))
+
+
+def attend_workspace_bytes(cfg: Config, args: AttendArgs) -> int:
+    """Bytes of workspace that a call with these sizes needs (0: none)."""
+    n = int(lib().spec_verify_attend_workspace_bytes(ctypes.byref(cfg), ctypes.byref(args)))
+    if n < 0:
+        raise SpecVerifyError(n, "spec_verify_attend_workspace_bytes")
+    return n
+
+
 def run_noalloc(cfg: Config, args: Args, stream: Optional[int] = None) -> None:
     """Enqueue one step without a handle: the library's static per-device
     workspace, no device allocation (see spec_verify_run_noalloc)."""
@@ -389,6 +531,26 @@ class SpecVerify:
     def head(self, args: HeadArgs, stream: Optional[int] = None) -> None:
         """Enqueue the 4-bit output head on ``stream``."""
         self._enqueue("spec_verify_head", args, stream)
+
+    def pages(self, args: PagesArgs, stream: Optional[int] = None) -> None:
+        """Enqueue a change of which slot of the cache holds which pages on ``stream``."""
+        self._enqueue("spec_verify_pages", args, stream)
+
+    def pages_copy(self, args: PagesCopyArgs, stream: Optional[int] = None) -> None:
+        """Enqueue copies of pages in every pool on ``stream``."""
+        self._enqueue("spec_verify_pages_copy", args, stream)
+
+    def append(self, args: AppendArgs, stream: Optional[int] = None) -> None:
+        """Enqueue the storing of new rows' keys and values on ``stream``."""
+        self._enqueue("spec_verify_append", args, stream)
+
+    def attend_workspace_bytes(self, args: AttendArgs) -> int:
+        """Bytes of workspace that ``attend`` needs for calls of these sizes."""
+        return attend_workspace_bytes(self.cfg, args)
+
+    def attend(self, args: AttendArgs, stream: Optional[int] = None) -> None:
+        """Enqueue the attention of a block's rows over the paged cache on ``stream``."""
+        self._enqueue("spec_verify_attend", args, stream)
 
     def timing_begin(self, max_calls: int) -> None:
         rc = lib().spec_verify_timing_begin(self._h, int(max_calls))

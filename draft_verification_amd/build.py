@@ -9,7 +9,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.hip", "sv_rules.hip", "sv_head.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.hip", "sv_rules.hip", "sv_head.hip", "sv_pages.hip", "sv_attend.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspec_verify.so")
 

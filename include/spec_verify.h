@@ -532,6 +532,236 @@ int spec_verify_head_pack(spec_verify_t* h, const spec_verify_head_pack_args* a,
 int spec_verify_head_check(const spec_verify_config* cfg, const spec_verify_head_args* a);
 int spec_verify_head(spec_verify_t* h, const spec_verify_head_args* a, void* hip_stream);
 
+/*
+ * The target's cache around verification.  One step of the target reads the
+ * cache of every sequence, adds the rows of its block to it, and keeps of them
+ * what verification accepts:
+ *   pages (reserve) -> for every layer: append, attend -> head -> process ->
+ *   spec_verify_run -> history, pages (commit, with accepted_len as last_row).
+ * Errors, streams, capture and overlap as for the calls around verification
+ * above: arguments are checked on the host, kernels are only enqueued, nothing
+ * of the handle but its configuration is used (of that the device, max_batch
+ * and max_draft).
+ *
+ * A sequence's tokens lie in pages of page_size tokens: token t of a slot at
+ * place t % page_size of page page_table[slot][t / page_size], in every layer.
+ * lengths[slot] is how many tokens the slot has for good (committed ones); the
+ * rows of the step in hand lie behind them, row r of a sequence at position
+ * lengths[slot] + row0 + r.  Row 0 of a verified block is the token that the
+ * step before emitted last, rows 1..K the drafted ones; a drafting step is one
+ * row, with row0 the number of tokens drafted before it.
+ *
+ * Rows: sequence b has `rows` of them, or with last_row (device int32 [B], as
+ * verify_len and accepted_len are) rows 0 .. last_row[b], at most `rows` (-1:
+ * none), or with row_offsets those of a packed batch, row_offsets[b] ..
+ * row_offsets[b+1]-1, at most `rows`.  slots[b] is its slot (-1: a padded
+ * sequence, nothing is done); NULL: slot b.
+ *
+ * device_status: optional int32 [1], 0 or SV_STATUS_* bits.  SV_STATUS_BAD_INPUT:
+ * a slot outside [-1, n_slots), a last_row below -1, row offsets that are
+ * negative, descending or further apart than `rows`, a negative length, or rows
+ * behind the pages that the slot holds (nothing is done for the sequence); a
+ * page outside [0, n_pages) in a table (what would lie there is not written, and
+ * not seen).  No call reads or writes outside the given buffers for any of them.
+ */
+#define SV_MAX_PAGES (1 << 24)
+#define SV_MAX_PAGE_SIZE 1024
+#define SV_MAX_CACHE_TOKENS (1 << 30)
+#define SV_MAX_PAGE_BATCH 4096
+#define SV_MAX_PAGE_ROWS (1 << 20)
+#define SV_MAX_HEAD_DIM 256
+enum { SV_STATUS_NO_PAGES = 4 }; /* a device_status bit: not every sequence got its pages */
+
+typedef struct {
+    int32_t n_slots;                /* 1 .. SV_MAX_BATCH; >= B without slots */
+    int32_t n_pages;                /* 1 .. SV_MAX_PAGES */
+    int32_t page_size;              /* tokens of a page: a power of two up to SV_MAX_PAGE_SIZE */
+    int32_t max_pages;              /* entries of a slot's table; max_pages * page_size <= SV_MAX_CACHE_TOKENS */
+    int32_t* page_table;            /* device [n_slots][max_pages] */
+    int32_t* lengths;               /* device [n_slots] */
+    int32_t* page_counts;           /* device [n_slots]: entries of the table in use.  NULL for append and attend: all */
+    int32_t* page_refs;             /* device [n_pages]: how many entries of tables name the page (pages only) */
+    uint32_t* free_pages;           /* device [ceil(n_pages / 32)]: bit p % 32 of word p / 32 set where page_refs[p]
+                                       is 0 (pages only) */
+} spec_verify_cache;
+
+/*
+ * Pages: which slot holds which pages.  One call does one kind of thing for B
+ * sequences:
+ *   SV_PAGES_CLEAR    every slot is emptied and every page free (B and slots are
+ *                     not looked at): the state to start from.
+ *   SV_PAGES_RESERVE  each slot gets the pages that `rows` (or last_row[b] + 1)
+ *                     rows behind its length need and it does not hold yet: the
+ *                     lowest free pages, in the order of b.  granted[b] = 1, or 0
+ *                     where the sequences up to b need more than there are free
+ *                     pages (this one then gets none, SV_STATUS_NO_PAGES).
+ *   SV_PAGES_COMMIT   lengths[slot] grows by `rows` (or last_row[b] + 1), and the
+ *                     pages behind it are given back.
+ *   SV_PAGES_RELEASE  the slot's length is 0 and all its pages are given back.
+ *   SV_PAGES_FORK     slots[b], which holds nothing, gets the tokens of
+ *                     from_slots[b]: it shares the full pages, and for a last page
+ *                     that is not full it gets the lowest free one, in the order of
+ *                     b; copies[b] = {that page, the new one} for
+ *                     spec_verify_pages_copy, or {-1, -1}.  granted[b] as for
+ *                     SV_PAGES_RESERVE; a slot that is not granted stays empty.
+ *                     Reserved pages behind the length are not shared.
+ *   SV_PAGES_COMPACT  with n pages in use, those at n and above move below it,
+ *                     the highest to the lowest free place and so on, at most
+ *                     max_copies of them: tables, page_refs and free_pages name
+ *                     the new places at once and copies lists {from, to}, filled
+ *                     up with {-1, -1}.  (B and slots are not looked at.)
+ * A page that is given back loses one of its references and is free when it has
+ * none; its entry in the table becomes -1.  Only rows behind the length are ever
+ * written, and those never lie in a shared page.
+ * A sequence whose slot another of the call names too (as from_slots, another's
+ * slot) is bad, and so is a fork to a slot that is not empty or from one whose
+ * length its pages do not hold: granted 0, nothing changed.  Deterministic: what a
+ * call does depends on its inputs alone.
+ */
+enum {
+    SV_PAGES_CLEAR = 0, SV_PAGES_RESERVE = 1, SV_PAGES_COMMIT = 2, SV_PAGES_RELEASE = 3, SV_PAGES_FORK = 4,
+    SV_PAGES_COMPACT = 5
+};
+
+typedef struct {
+    int32_t B;                      /* 0 <= B <= max_batch and SV_MAX_PAGE_BATCH */
+    int32_t kind;                   /* SV_PAGES_* */
+    spec_verify_cache cache;        /* every array of it */
+    const int32_t* slots;           /* optional device [B] */
+    const int32_t* from_slots;      /* FORK: device [B]; one slot may be forked many times */
+    int32_t rows;                   /* RESERVE, COMMIT: 0 .. SV_MAX_CACHE_TOKENS */
+    const int32_t* last_row;        /* RESERVE, COMMIT: optional device [B] */
+    int32_t* granted;               /* FORK: device [B], 1 or 0 (0 also for -1 as a slot, and for bad ones);
+                                       RESERVE: likewise, optional */
+    int32_t* copies;                /* FORK, COMPACT: device [max_copies][2] */
+    int32_t max_copies;             /* FORK: >= B (entries past B are not written); COMPACT: 0 .. SV_MAX_PAGES */
+    int32_t* device_status;         /* optional device [1] */
+} spec_verify_pages_args;
+
+int spec_verify_pages_check(const spec_verify_config* cfg, const spec_verify_pages_args* a);
+int spec_verify_pages(spec_verify_t* h, const spec_verify_pages_args* a, void* hip_stream);
+
+/*
+ * Copies pages in every pool (each layer's keys and values): in pool i,
+ * page_bytes bytes at pools + i * pool_stride + from * page_stride go to the
+ * place of `to`, for each pair {from, to} of copies.  Pairs with -1 in them are
+ * left out.  No page is written twice, nor both read and written, as with the
+ * lists that spec_verify_pages makes.  Everything is a multiple of 16 bytes.
+ * Pages outside [0, n_pages) are bad (left out).
+ */
+typedef struct {
+    int32_t n_copies;               /* 0 .. SV_MAX_PAGES */
+    const int32_t* copies;          /* device [n_copies][2] */
+    void* pools;                    /* device */
+    int32_t n_pools;                /* 1 .. 65535 */
+    int64_t pool_stride;            /* bytes; >= n_pages * page_stride (one pool: not looked at) */
+    int64_t page_stride;            /* bytes; >= page_bytes */
+    int64_t page_bytes;
+    int32_t n_pages;                /* 1 .. SV_MAX_PAGES */
+    int32_t* device_status;         /* optional device [1] */
+} spec_verify_pages_copy_args;
+
+int spec_verify_pages_copy_check(const spec_verify_config* cfg, const spec_verify_pages_copy_args* a);
+int spec_verify_pages_copy(spec_verify_t* h, const spec_verify_pages_copy_args* a, void* hip_stream);
+
+/*
+ * Keys and values of one layer: element (page, head, place, d) at keys (values) +
+ * page * page_stride + head * head_stride + place * token_stride + d, so that a
+ * page may hold its tokens head by head or token by token.
+ *   SV_KV_BF16  held in bf16.
+ *   SV_KV_E4M3  held in 8 bits: a code stands for its value (e4m3: 1 sign, 4
+ *               exponent, 3 fraction bits, largest 448, no infinities) times the
+ *               scale of its head.
+ */
+enum { SV_KV_BF16 = 0, SV_KV_E4M3 = 1 };
+
+typedef struct {
+    int32_t kv_heads;               /* 1 .. 1024 */
+    int32_t head_dim;               /* a multiple of 16 up to SV_MAX_HEAD_DIM */
+    int32_t type;                   /* SV_KV_BF16 | SV_KV_E4M3 */
+    void* keys;                     /* device, 16-byte aligned, as each row in it is */
+    void* values;
+    int64_t page_stride, head_stride, token_stride; /* elements; each >= head_dim and a multiple of 16 bytes */
+    const float* key_scales;        /* E4M3: device [kv_heads], finite and > 0; NULL: 1 */
+    const float* value_scales;
+} spec_verify_kv;
+
+/*
+ * Append: stores the keys and values of a step's rows in their pages, bf16 as
+ * they are, or with SV_KV_E4M3 as the code nearest to x / scale (fp32 division,
+ * ties to even; beyond +-448 the largest code; NaN stays NaN).  Row r of a dense
+ * batch is read at keys (values) + b * batch_stride + r * row_stride + head *
+ * head_stride, of a packed batch at (row_offsets[b] + r) * row_stride (elements;
+ * any alignment of bf16, 16-byte aligned rows are fastest).  A row whose page is
+ * bad is not stored.  Two sequences must not name one slot with common rows.
+ */
+typedef struct {
+    int32_t B, rows;                /* 0 <= B <= max_batch; 1 <= rows <= SV_MAX_PAGE_ROWS */
+    int32_t row0;                   /* 0 .. SV_MAX_PAGE_ROWS */
+    spec_verify_cache cache;        /* page_table and lengths; page_counts optional */
+    spec_verify_kv kv;              /* written */
+    const int32_t* slots;           /* optional device [B] */
+    const int32_t* last_row;        /* optional device [B] (dense rows only) */
+    const int64_t* row_offsets;     /* optional device [B+1]: packed rows */
+    const void* keys;               /* device bf16 */
+    const void* values;
+    int64_t batch_stride, row_stride, head_stride; /* of both; row and head >= head_dim */
+    int32_t* device_status;         /* optional device [1] */
+} spec_verify_append_args;
+
+int spec_verify_append_check(const spec_verify_config* cfg, const spec_verify_append_args* a);
+int spec_verify_append(spec_verify_t* h, const spec_verify_append_args* a, void* hip_stream);
+
+/*
+ * Attend: attention of the rows of every sequence's block over its cache, the
+ * block's own rows (appended before) among it.  Row r at position p = lengths +
+ * row0 + r sees the positions t <= p, with a window only the last `window` of
+ * them; head h reads key-value head h / (heads / kv_heads):
+ *   s_t = scale * <q, k_t>,  out = sum_t exp(s_t - lse) v_t,  lse = ln sum_t exp(s_t)
+ * Queries and outputs are bf16, lse fp32.  Products are exact in fp32 (keys of
+ * SV_KV_E4M3 meet their scale after the sum) and summed in fp32, as the softmax
+ * is; the weights exp(s_t - max) are rounded to bf16 for their product with the
+ * values, the sum that divides them is taken before.  A row that sees nothing
+ * (bad pages) is 0 and its lse -infinity.  What a row does not see, later rows of its
+ * own block among it, does not change its result, infinities and NaN included.  Rows
+ * that are not there keep their contents in both outputs.
+ *
+ * The length of a sequence is split over workgroups, whose parts are joined in a
+ * fixed order: results are the same from run to run, but may differ in their last
+ * bits with B, rows and max_len, which decide how it is split.
+ *
+ * workspace: spec_verify_attend_workspace_bytes(cfg, a) bytes, 16-byte aligned, the
+ * caller's (it may be 0; a larger one will do).  Calls that overlap, and graphs that
+ * may be replayed at once, need one each.
+ */
+typedef struct {
+    int32_t B, rows;                /* 0 <= B <= max_batch; 1 <= rows; row0 + rows <= max_draft + 1 */
+    int32_t row0;                   /* >= 0 */
+    spec_verify_cache cache;        /* page_table and lengths; page_counts optional */
+    spec_verify_kv kv;
+    const int32_t* slots;           /* optional device [B] */
+    const int32_t* last_row;        /* optional device [B] (dense rows only) */
+    const int64_t* row_offsets;     /* optional device [B+1]: packed rows */
+    int32_t heads;                  /* a multiple of kv_heads, up to 64 times as many */
+    const void* queries;            /* device bf16; element (b, r, h, d) as append's rows are */
+    int64_t query_batch_stride, query_row_stride, query_head_stride;
+    void* outputs;                  /* device bf16, likewise; no overlap with the queries */
+    int64_t output_batch_stride, output_row_stride, output_head_stride;
+    float* lse;                     /* optional device [B][rows][heads], or of packed rows [row][heads] */
+    float scale;                    /* finite */
+    int32_t window;                 /* 0: none */
+    int32_t max_len;                /* the caller's promise that lengths + row0 + rows <= max_len, of the sequences' own
+                                       rows, which spares workgroups; 0: max_pages * page_size.  A longer sequence is bad. */
+    void* workspace;
+    int64_t workspace_bytes;
+    int32_t* device_status;         /* optional device [1] */
+} spec_verify_attend_args;
+
+/* Bytes that a call with these sizes needs (buffers are not looked at), or a negative status. */
+int64_t spec_verify_attend_workspace_bytes(const spec_verify_config* cfg, const spec_verify_attend_args* a);
+int spec_verify_attend_check(const spec_verify_config* cfg, const spec_verify_attend_args* a);
+int spec_verify_attend(spec_verify_t* h, const spec_verify_attend_args* a, void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

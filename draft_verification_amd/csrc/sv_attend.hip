@@ -65,6 +65,14 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// A barrier for LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // The tokens that a sequence's rows see, and how they are split.
 struct Reach {
     int low, end; // low: a multiple of the tile
@@ -104,10 +112,13 @@ __device__ __forceinline__ unsigned widen_e4m3(unsigned codes)
     return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HIGH));
 }
 
-// Whether one of two bf16 is infinite or NaN.
-__device__ __forceinline__ bool special2(unsigned w)
+// Whether one of eight bf16 is infinite or NaN.
+__device__ __forceinline__ bool special4(u32x4 w)
 {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    bool is = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) is |= ((w[j] & 0x7f80u) == 0x7f80u) | ((w[j] & 0x7f800000u) == 0x7f800000u);
+    return is;
 }
 
 __device__ __forceinline__ unsigned without_special(unsigned w)
@@ -123,31 +134,37 @@ __device__ __forceinline__ unsigned without_special(unsigned w)
 // row's scores of four tokens in each of two tiles; rounded, these are in place as
 // the right operand of out^T = V^T P^T, whose left operand LDS reads transposed.  A
 // row's maximum is not followed at every step: its reference stays as long as no
-// score lies more than 8 (in log2) above it, which keeps the weights below 2^8 and
-// spares the sums' rescaling.
+// score lies more than 16 (in log2) above it, which keeps the weights below 2^16 and
+// spares the sums' rescaling (bf16 holds such weights as well as those below 1).
 //
-// The four wavefronts take every fourth tile of 32 tokens, each through its own part
-// of LDS and with registers one tile ahead, without a barrier until the end, where
-// their sums are joined.
-template <int DIM, bool E4M3, int TILES>
-__global__ __launch_bounds__(kThreads, DIM == 64 && TILES == 1 ? 4 : (DIM == 128 && TILES <= 3) || DIM == 64 ? 2 : 1) void sv_attend_kernel(Attend q)
+// SHARED = false, for few rows: the four wavefronts take every fourth tile of 32 tokens,
+// each through its own part of LDS and with registers one tile ahead, without a barrier
+// until the end, where their sums are joined.
+// SHARED = true, for many rows: each wavefront has rows of its own and they share a tile
+// of 64 tokens in LDS, so that no sums are held twice.
+template <int DIM, bool E4M3, int TILES, bool SHARED>
+__global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 : DIM < 256 ? 2 : 1) void sv_attend_kernel(Attend q)
 {
     constexpr int kUnit = E4M3 ? 16 : 8;           // values of 16 bytes of the cache
     constexpr int kLanes = DIM / kUnit;            // lanes that read a token's row
-    constexpr int kPer = 64 / kLanes;              // tokens of a load
-    constexpr int kLoads = kAttendTokens / kPer;   // loads of a tile, of keys and of values each
-    constexpr int kChunks = DIM / 8;               // 16 bytes of bf16
+    constexpr int kTile = SHARED ? 2 * kAttendTokens : kAttendTokens; // tokens in LDS at a time
+    constexpr int kPer = (SHARED ? kThreads : 64) / kLanes; // tokens of a round of loads
+    constexpr int kLoads = kTile / kPer;           // rounds of a tile, of keys and of values each
     constexpr int kSteps = DIM / 32;               // products of a score
     constexpr int kOut = DIM / 16;                 // tiles of a row of outputs
-    constexpr int kTileBytes = kAttendTokens * DIM * 2;
-    constexpr bool kQueryLds = TILES > 2;
+    constexpr int kRows = TILES * 16 * (SHARED ? kAttendWaves : 1); // of the workgroup
+    constexpr int kTileBytes = kTile * DIM * 2;
+    constexpr bool kTwo = SHARED;                  // keys and values in LDS of their own
+    constexpr bool kQueryLds = SHARED ? TILES > (DIM > 128 ? 0 : 1) : TILES > 1;
     constexpr int kMergeRow = DIM + 4;             // floats of a row where the sums meet
-    constexpr int kStage = kAttendWaves * kTileBytes;
-    constexpr int kMerge = kAttendWaves * 16 * kMergeRow * 4;
+    constexpr int kStage = SHARED ? 2 * kTileBytes : kAttendWaves * kTileBytes;
+    constexpr int kMerge = SHARED ? 0 : kAttendWaves * 16 * kMergeRow * 4;
+    constexpr int kStride = SHARED ? kTile : kTile * kAttendWaves;
     __shared__ __attribute__((aligned(16))) char stage[kStage > kMerge ? kStage : kMerge];
-    __shared__ u32x4 query[kQueryLds ? TILES * kSteps * 64 : 1];
-    __shared__ int place[TILES * 16];              // position of each row
-    __shared__ float refs[kAttendWaves][TILES * 16], sums[kAttendWaves][TILES * 16];
+    __shared__ u32x4 query[kQueryLds ? kRows / 16 * kSteps * 64 : 1];
+    __shared__ int place[kRows];                   // position of each row
+    __shared__ unsigned noted[kRows * kOut];       // infinities beside the sums: bit 2i of column i, bit 2i + 1 the negative one; both: NaN
+    __shared__ float refs[kAttendWaves][SHARED ? 1 : kRows], sums[kAttendWaves][SHARED ? 1 : kRows];
 
     const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -173,10 +190,12 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && TILES == 1 ? 4 : (DIM == 128
     }
     const Reach reach = reach_of(q, s);
     if (split >= reach.splits) return;
-    const int row0 = block * TILES * 16;           // first row (of a row and a head) of the workgroup
+    const int row0 = block * kRows;                // first row (of a row and a head) of the workgroup
     const int rows = s.count * q.group - row0;     // and how many there are
     if (rows <= 0) return;
     const int first = reach.low + split * q.span, last = min(first + q.span, reach.end);
+    const int tile0 = SHARED ? wave * TILES : 0;   // first tile of the wavefront's rows
+    const int tiles = min(TILES, (rows + 15) / 16 - tile0); // and how many there are (SHARED: maybe none)
 
     // the queries, negative for a negative scale, as right operands; rows past the last
     // are those of the last
@@ -184,7 +203,7 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && TILES == 1 ? 4 : (DIM == 128
     if (E4M3 && q.kscale) scale *= cache_uniform(q.kscale + head);
     const unsigned flip = scale < 0 ? 0x80008000u : 0u;
     scale = fabsf(scale);
-    const float room = 8.0f / scale;               // how far a score may lie above its reference
+    const float room = 16.0f / scale;              // how far a score may lie above its reference
     const bool followed = room < FLT_MAX;          // (a scale of about zero: the reference is 0)
     auto query_at = [&](int tile, int step) {
         const int m = min(tile * 16 + n16, rows - 1) + row0;
@@ -197,36 +216,43 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && TILES == 1 ? 4 : (DIM == 128
     };
     u32x4 qreg[kQueryLds ? 1 : TILES][kQueryLds ? 1 : kSteps];
     if constexpr (kQueryLds) {
-        for (int i = wave; i < TILES * kSteps; i += kAttendWaves) query[i * 64 + lane] = query_at(i / kSteps, i % kSteps);
+        for (int i = wave; i < kRows / 16 * kSteps; i += kAttendWaves) query[i * 64 + lane] = query_at(i / kSteps, i % kSteps);
     } else {
 #pragma unroll
         for (int i = 0; i < TILES; ++i)
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) qreg[i][k] = query_at(i, k);
+            for (int k = 0; k < kSteps; ++k) qreg[i][k] = query_at(tile0 + i, k);
     }
-    for (int i = threadIdx.x; i < TILES * 16; i += kThreads) place[i] = s.start + (min(i, rows - 1) + row0) / q.group;
+    for (int i = threadIdx.x; i < kRows * kOut; i += kThreads) noted[i] = 0;
+    for (int i = threadIdx.x; i < kRows; i += kThreads) place[i] = s.start + (min(i, rows - 1) + row0) / q.group;
 
-    // the wavefront's own LDS, for keys and then for values: a token's row of 16-byte chunks,
-    // their order changed from token to token so that a column of them lies in different banks
-    char* const own = stage + wave * kTileBytes;
-    auto key_at = [](int t, int chunk) { return t * DIM * 2 + ((chunk ^ ((DIM == 64 ? t >> 1 : t) & (kChunks < 16 ? 7 : 15))) * 16); };
-    auto value_at = [](int t, int half) { return t * DIM * 2 + ((half ^ ((DIM == 64 ? t >> 1 : t) & (kOut < 8 ? 3 : 7))) * 32); };
+    // keys and values in LDS: a token's row of 16-byte chunks, their order changed from token
+    // to token so that a column of them lies in different banks
+    char* const kt = stage + (SHARED ? 0 : wave * kTileBytes);
+    char* const vt = kTwo ? kt + kTileBytes : kt;
+    auto key_at = [](int t, int chunk) { return t * DIM * 2 + ((chunk ^ ((DIM == 64 ? t >> 1 : t) & (DIM < 128 ? 7 : 15))) * 16); };
+    auto value_at = [](int t, int half) { return t * DIM * 2 + ((half ^ ((DIM == 64 ? t >> 1 : t) & (DIM < 128 ? 3 : 7))) * 32); };
+    auto sync = [&] {
+        if constexpr (SHARED) lds_barrier();
+        else wave_sync();
+    };
 
-    const int in_load = lane / kLanes, unit = lane % kLanes;
-    const bool lane_in = unit * kUnit < q.dim;
-    const long long in_page = head * q.head_stride + (lane_in ? unit * 16 : 0);
     const int* table = q.c.table + (long long)s.slot * q.c.max_pages;
     const int mask = (1 << q.c.shift) - 1;
+    // which of a tile's tokens this lane loads in round 0, and which 16 bytes
+    const int loader = SHARED ? threadIdx.x : lane;
+    const bool lane_in = loader % kLanes * kUnit < q.dim;
+    const long long in_page = head * q.head_stride + (lane_in ? loader % kLanes * 16 : 0);
 
-    // the pages of a tile's tokens, a token to each of 32 lanes; those past the end are the last
-    auto pages_of = [&](int t0) { return table[min(t0 + (lane & 31), reach.end - 1) >> q.c.shift]; };
+    // the pages of a tile's tokens, a token to a lane; those past the end are the last
+    auto pages_of = [&](int t0) { return table[min(t0 + (lane & (kTile - 1)), reach.end - 1) >> q.c.shift]; };
     u32x4 kr[kLoads], vr[kLoads];
     auto is_bad = [&](int page) { return page < 0 || page >= q.c.n_pages; };
     auto load = [&](u32x4 (&x)[kLoads], const char* from, int t0, int page) { // of a bad page's tokens, the first page's
         if (is_bad(page)) page = 0;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int t = i * kPer + in_load;
+            const int t = i * kPer + loader / kLanes;
             x[i] = *(const u32x4*)(from + in_page + __shfl(page, t) * q.page_stride + (unsigned)(min(t0 + t, reach.end - 1) & mask) * (unsigned long long)q.token_stride);
         }
     };
@@ -240,68 +266,126 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && TILES == 1 ? 4 : (DIM == 128
 #pragma unroll
     for (int i = 0; i < TILES; ++i) ref[i] = followed ? -FLT_MAX : 0.0f, top[i] = followed ? -FLT_MAX : 0.0f, sum[i] = 0.0f;
 
-    const int stride = kAttendTokens * kAttendWaves;
-    int t0 = first + wave * kAttendTokens;
+    int t0 = first + (SHARED ? 0 : wave * kTile);
     int page = 0, next_page = 0; // of a token of the tile in hand and of the next
     if (t0 < last) {
         page = pages_of(t0);
         load(kr, q.keys, t0, page);
         load(vr, q.values, t0, page);
-        next_page = pages_of(t0 + stride);
+        next_page = pages_of(t0 + kStride);
     }
     __syncthreads(); // queries and places
-    for (; t0 < last; t0 += stride) {
-        const bool more = t0 + stride < last;
-        const unsigned gone = (unsigned)__ballot(is_bad(page)); // tokens whose page is bad
+    for (; t0 < last; t0 += kStride) {
+        const bool more = t0 + kStride < last;
+        // with many sums to hold, places in LDS are worked out anew rather than kept
+        int lane_ = lane;
+        if constexpr (TILES > 1) asm volatile("" : "+v"(lane_));
+        const int n16 = lane_ & 15, g = lane_ >> 4;
+        const int loader = SHARED ? wave * 64 + lane_ : lane_, in_load = loader / kLanes, unit = loader % kLanes;
+        const unsigned long long gone = __ballot(is_bad(page)); // tokens whose page is bad
         if (gone && lane == 0) cache_status(q.status, SV_STATUS_BAD_INPUT);
         // some row does not see some token
-        const bool mixed = t0 + kAttendTokens - 1 > s.start || gone || (q.window && t0 <= s.start + s.count - 1 - q.window);
+        const bool mixed = t0 + kTile - 1 > s.start || gone || (q.window && t0 <= s.start + s.count - 1 - q.window);
+        bool odd = false; // whether a value of a mixed tile is infinite or NaN
+        auto store_keys = [&] {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
+            for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-            for (int k = 0; k < kUnit / 8; ++k)
-                *(u32x4*)(own + key_at(i * kPer + in_load, unit * (kUnit / 8) + k)) = lane_in ? widen(kr[i], k) : u32x4{0, 0, 0, 0};
-        if (more) load(kr, q.keys, t0 + stride, next_page);
-        wave_sync();
-        bf16x8 k[2][kSteps];
+                for (int k = 0; k < kUnit / 8; ++k)
+                    *(u32x4*)(kt + key_at(i * kPer + in_load, unit * (kUnit / 8) + k)) = lane_in ? widen(kr[i], k) : u32x4{0, 0, 0, 0};
+            if (more) load(kr, q.keys, t0 + kStride, next_page);
+        };
+        auto store_values = [&] {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-            for (int e = 0; e < kSteps; ++e) k[u][e] = *(const bf16x8*)(own + key_at(u * 16 + n16, e * 4 + g));
-        u32x4 p[TILES];
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-            f32x4 x[2] = {};
-#pragma unroll
-            for (int e = 0; e < kSteps; ++e) {
-                bf16x8 y;
-                if constexpr (kQueryLds) y = __builtin_bit_cast(bf16x8, query[(i * kSteps + e) * 64 + lane]);
-                else y = __builtin_bit_cast(bf16x8, qreg[i][e]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][e], y, x[u], 0, 0, 0);
+                for (int k = 0; k < kUnit / 8; ++k) {
+                    const int chunk = unit * (kUnit / 8) + k;
+                    const u32x4 v = lane_in ? widen(vr[i], k) : u32x4{0, 0, 0, 0};
+                    if (mixed) odd |= special4(v);
+                    *(u32x4*)(vt + value_at(i * kPer + in_load, chunk / 2) + chunk % 2 * 16) = v;
+                }
+            if (more) load(vr, q.values, t0 + kStride, next_page);
+        };
+        // A weight of zero does not hide an infinity or a NaN from rows that do not see its
+        // token.  Such values are noted for the rows that do, and taken as zero.
+        auto take_out = [&] {
+            if constexpr (SHARED) odd = __syncthreads_or(odd);
+            else odd = __ballot(odd) != 0;
+            if (!odd) return;
+            for (int in = SHARED ? wave : 0; in < kTile && t0 + in < reach.end; in += SHARED ? kAttendWaves : 1) {
+                const int t = t0 + in;
+                if (gone >> in & 1) continue;
+                for (int d = lane; d < q.dim; d += 64) {
+                    const unsigned x = *(const unsigned short*)(vt + value_at(in, d / 16) + d % 16 * 2);
+                    if ((x & 0x7f80u) != 0x7f80u) continue;
+                    const unsigned kind = (x & 0x7fu ? 3u : x & 0x8000u ? 2u : 1u) << (d % 16 * 2);
+                    for (int m = 0; m < rows && m < kRows; ++m)
+                        if (t <= place[m] && (!q.window || t > place[m] - q.window)) atomicOr(&noted[m * kOut + d / 16], kind);
+                }
             }
-            unsigned hidden = 0; // bit u * 4 + j
-            if (mixed) {
-                const int at = place[i * 16 + n16], low = q.window ? at - q.window : -1;
+            sync();
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int in = u * 16 + g * 4 + j, t = t0 + in;
-                        if (t > at || t <= low || (gone >> in & 1)) {
-                            hidden |= 1u << (u * 4 + j);
-                            x[u][j] = -FLT_MAX;
+                for (int k = 0; k < kUnit / 8; ++k) {
+                    const int chunk = unit * (kUnit / 8) + k;
+                    u32x4* const at = (u32x4*)(vt + value_at(i * kPer + in_load, chunk / 2) + chunk % 2 * 16);
+                    u32x4 v = *at;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = without_special(v[j]);
+                    *at = v;
+                }
+            sync();
+        };
+        store_keys();
+        if constexpr (kTwo) store_values();
+        sync();
+        if (kTwo && mixed) take_out();
+#pragma unroll
+        for (int part = 0; part < kTile / kAttendTokens; ++part) { // 32 tokens at a time
+            if (part && t0 + part * kAttendTokens >= last) break;
+            const int in_tile = part * kAttendTokens;
+            bf16x8 k[2][kSteps];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) k[u][e] = *(const bf16x8*)(kt + key_at(in_tile + u * 16 + n16, e * 4 + g));
+            u32x4 p[TILES] = {};
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                if (SHARED && i >= tiles) break;
+                f32x4 x[2] = {};
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) {
+                    bf16x8 y;
+                    if constexpr (kQueryLds) y = __builtin_bit_cast(bf16x8, query[((tile0 + i) * kSteps + e) * 64 + lane_]);
+                    else y = __builtin_bit_cast(bf16x8, qreg[i][e]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][e], y, x[u], 0, 0, 0);
+                }
+                unsigned hidden = 0; // bit u * 4 + j
+                if (mixed) {
+                    const int at = place[(tile0 + i) * 16 + n16], low = q.window ? at - q.window : -1;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int in = in_tile + u * 16 + g * 4 + j, t = t0 + in;
+                            if (t > at || t <= low || (gone >> in & 1)) {
+                                hidden |= 1u << (u * 4 + j);
+                                x[u][j] = -FLT_MAX;
+                            }
                         }
-                    }
-            }
-            if (followed) {
-                float most = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
-                if (__ballot(most > ref[i] + room)) {
-                    most = fmaxf(most, __shfl_xor(most, 16));
-                    most = fmaxf(most, __shfl_xor(most, 32));
-                    most = fmaxf(most, ref[i]);
-                    if (most > ref[i]) {
-                        const float now = most * scale, factor = exp2_of(top[i] - now);
+                }
+                if (followed) {
+                    float most = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+                    if (__ballot(most > ref[i] + room)) {
+                        most = fmaxf(most, __shfl_xor(most, 16));
+                        most = fmaxf(most, __shfl_xor(most, 32));
+                        most = fmaxf(most, ref[i]);
+                        // (every lane takes part: sums that only some lanes change would be held twice)
+                        const float now = most > ref[i] ? most * scale : top[i], factor = exp2_of(top[i] - now);
                         ref[i] = most;
                         top[i] = now;
                         sum[i] *= factor;
@@ -309,151 +393,135 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && TILES == 1 ? 4 : (DIM == 128
                         for (int e = 0; e < kOut; ++e) acc[i][e] *= factor;
                     }
                 }
-            }
-            float w[8];
+                float w[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = exp2_of(fmaf(x[j / 4][j % 4], scale, -top[i]));
-            if (mixed) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (hidden >> j & 1) w[j] = 0.0f;
-            }
-            sum[i] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-            // rounded to bf16, as the matrix cores take them: half a step of 2^-8 each, as the
-            // outputs' own rounding is
-            p[i] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
-        }
-        wave_sync(); // the keys are read
-        bool odd = false; // infinities or NaN among the values of a mixed tile
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-            for (int k = 0; k < kUnit / 8; ++k) {
-                const int chunk = unit * (kUnit / 8) + k;
-                u32x4 v = lane_in ? widen(vr[i], k) : u32x4{0, 0, 0, 0};
+                for (int j = 0; j < 8; ++j) w[j] = exp2_of(fmaf(x[j / 4][j % 4], scale, -top[i]));
                 if (mixed) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) odd |= special2(v[j]), v[j] = without_special(v[j]);
+                    for (int j = 0; j < 8; ++j)
+                        if (hidden >> j & 1) w[j] = 0.0f;
                 }
-                *(u32x4*)(own + value_at(i * kPer + in_load, chunk / 2) + chunk % 2 * 16) = v;
+                sum[i] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+                // rounded to bf16, as the matrix cores take them: half a step of 2^-8 each, as the
+                // outputs' own rounding is
+                p[i] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
+                if constexpr (TILES > 1) __builtin_amdgcn_sched_barrier(0); // one tile after the other, or their scores pile up and spill
             }
-        if (more) load(vr, q.values, t0 + stride, next_page);
-        wave_sync();
-#pragma unroll
-        for (int e = 0; e < kOut; ++e) {
-            // values of four tokens of each half, a column to each lane
-            s16x4 v[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = u * 16 + g * 4 + n16 / 4;
-                v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(own + value_at(t, e) + n16 % 4 * 8));
+            if constexpr (!kTwo) {
+                sync(); // the keys are read
+                store_values();
+                sync();
+                if (mixed) take_out();
             }
-            const u32x2 lo = __builtin_bit_cast(u32x2, v[0]), hi = __builtin_bit_cast(u32x2, v[1]);
-            const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, p[i]), acc[i][e], 0, 0, 0);
-        }
-        if (mixed && __ballot(odd)) {
-            // Values that are infinite or NaN were taken as zero, since a weight of zero does not
-            // hide them from rows that do not see their token.  They are added one by one.
+            for (int e = 0; e < kOut; ++e) {
+                // values of four tokens of each half, a column to each lane: tokens u * 16 + g * 4 + j
+                s16x4 v[2];
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                wave_sync();
-                ((u32x4*)own)[lane] = p[i];
-                wave_sync();
-                const int at = place[i * 16 + n16], low = q.window ? at - q.window : -1;
-                for (int in = 0; in < kAttendTokens && t0 + in < reach.end; ++in) {
-                    const int t = t0 + in;
-                    if (gone >> in & 1) continue;
-                    const unsigned short* const all = (const unsigned short*)own;
-                    const float w = __uint_as_float((unsigned)all[(in % 16 / 4 * 16 + n16) * 8 + in / 16 * 4 + in % 4] << 16);
-                    const bool sees = t <= at && t > low;
-                    const char* from = q.values + head * q.head_stride + table[t >> q.c.shift] * q.page_stride + (unsigned)(t & mask) * (unsigned long long)q.token_stride;
-#pragma unroll
-                    for (int e = 0; e < kOut; ++e) {
-                        const int d = e * 16 + g * 4;
-                        if (!sees || d >= q.dim) continue;
-                        unsigned x[2];
-                        if constexpr (E4M3) {
-                            const unsigned codes = *(const unsigned*)(from + d);
-                            x[0] = widen_e4m3<false>(codes), x[1] = widen_e4m3<true>(codes);
-                        } else {
-                            const u32x2 raw = *(const u32x2*)(from + 2 * d);
-                            x[0] = raw[0], x[1] = raw[1];
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const unsigned bits = j % 2 ? x[j / 2] & 0xffff0000u : x[j / 2] << 16;
-                            if ((bits & 0x7f800000u) == 0x7f800000u) acc[i][e][j] += w * __uint_as_float(bits);
-                        }
-                    }
+                for (int u = 0; u < 2; ++u) {
+                    const int t = in_tile + u * 16 + g * 4 + n16 / 4;
+                    v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + value_at(t, e) + n16 % 4 * 8));
                 }
+                const u32x2 lo = __builtin_bit_cast(u32x2, v[0]), hi = __builtin_bit_cast(u32x2, v[1]);
+                const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+#pragma unroll
+                for (int i = 0; i < TILES; ++i)
+                    acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, p[i]), acc[i][e], 0, 0, 0);
             }
         }
-        wave_sync(); // the values are read
+        sync(); // the tile is read
         page = next_page;
-        if (more) next_page = pages_of(t0 + 2 * stride);
+        if (more) next_page = pages_of(t0 + 2 * kStride);
     }
 
-    // the four wavefronts' sums, a tile of rows at a time
+    const float vscale = E4M3 && q.vscale ? cache_uniform(q.vscale + head) : 1.0f;
+    const bool whole = reach.splits == 1;
+    float* const parts = q.parts + (((long long)b * q.kv_heads + head) * q.blocks + block) * ((long long)q.splits * (kRows * (DIM + 2)))
+                       + (long long)split * (kRows * (DIM + 2));
+    // stores four columns of row m of the workgroup, with what was noted for them
+    auto put = [&](int m, int d, f32x4 x, float all) {
+        const unsigned also = noted[m * kOut + d / 16] >> (d % 16 * 2) & 0xffu;
+        if (also) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (also >> 2 * j & 1) x[j] += INFINITY;
+                if (also >> 2 * j & 2) x[j] -= INFINITY;
+            }
+        }
+        if (!whole) {
+            *(f32x4*)(parts + m * DIM + d) = x;
+        } else if (d < q.dim) {
+            const int row = (m + row0) / q.group, h = head * q.group + (m + row0) % q.group;
+            const float by = all == 0.0f ? 0.0f : vscale / all;
+            unsigned short* to = q.out + (q.r.roff ? (s.first + row) * q.orow : b * q.ob + row * q.orow) + h * q.oh + d;
+            *(u32x2_any*)to = u32x2{pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by)};
+        }
+    };
+    auto put_sum = [&](int m, float most, float all) {
+        if (!whole) {
+            parts[kRows * DIM + 2 * m] = most;
+            parts[kRows * DIM + 2 * m + 1] = all;
+        } else if (q.lse) {
+            const int row = (m + row0) / q.group, h = head * q.group + (m + row0) % q.group;
+            const long long line = q.r.roff ? s.first + row : (long long)b * q.r.rows + row;
+            q.lse[line * (q.kv_heads * q.group) + h] = all == 0.0f ? -INFINITY : (most + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f;
+        }
+    };
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
         sum[i] += __shfl_xor(sum[i], 16);
         sum[i] += __shfl_xor(sum[i], 32);
-        if (g == 0) refs[wave][i * 16 + n16] = top[i], sums[wave][i * 16 + n16] = sum[i];
     }
-    float* const meet = (float*)stage;
-    const float vscale = E4M3 && q.vscale ? cache_uniform(q.vscale + head) : 1.0f;
-    const bool whole = reach.splits == 1;
-    float* const parts = q.parts + (((long long)(b * (long long)q.kv_heads + head) * q.blocks + block) * q.splits + split) * (TILES * 16 * (DIM + 2));
+    if constexpr (SHARED) {
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) {
-        if (i * 16 >= rows) break;
-        __syncthreads();
+        for (int i = 0; i < TILES; ++i) {
+            const int m = (tile0 + i) * 16 + n16;
+            if (m >= rows) continue;
 #pragma unroll
-        for (int e = 0; e < kOut; ++e) *(f32x4*)(meet + (wave * 16 + n16) * kMergeRow + e * 16 + g * 4) = acc[i][e];
-        __syncthreads();
-        const int r = threadIdx.x / 16, m = i * 16 + r;
-        float most = refs[0][m];
-#pragma unroll
-        for (int w = 1; w < kAttendWaves; ++w) most = fmaxf(most, refs[w][m]);
-        float factor[kAttendWaves], all = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAttendWaves; ++w) {
-            factor[w] = exp2_of(refs[w][m] - most);
-            all += factor[w] * sums[w][m];
+            for (int e = 0; e < kOut; ++e) put(m, e * 16 + g * 4, acc[i][e], sum[i]);
+            if (g == 0) put_sum(m, top[i], sum[i]);
         }
-        if (m >= rows) continue;
-        const int full = m + row0, row = full / q.group, h = head * q.group + full % q.group;
-        const float by = whole ? (all == 0.0f ? 0.0f : vscale / all) : 1.0f;
-        const long long line = q.r.roff ? s.first + row : (long long)b * q.r.rows + row;
+    } else {
+        // the four wavefronts' sums, a tile of rows at a time
+        float* const meet = (float*)stage;
+        if (g == 0) {
 #pragma unroll
-        for (int e = 0; e < DIM / 64; ++e) {
-            const int d = e * 64 + threadIdx.x % 16 * 4;
-            f32x4 x = {};
-#pragma unroll
-            for (int w = 0; w < kAttendWaves; ++w) x += factor[w] * *(const f32x4*)(meet + (w * 16 + r) * kMergeRow + d);
-            if (!whole) {
-                *(f32x4*)(parts + m * DIM + d) = x;
-            } else if (d < q.dim) {
-                unsigned short* to = q.out + (q.r.roff ? line * q.orow : b * q.ob + row * q.orow) + h * q.oh + d;
-                *(u32x2_any*)to = u32x2{pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by)};
-            }
+            for (int i = 0; i < TILES; ++i) refs[wave][i * 16 + n16] = top[i], sums[wave][i * 16 + n16] = sum[i];
         }
-        if (threadIdx.x % 16 == 0) {
-            if (!whole) {
-                parts[TILES * 16 * DIM + 2 * m] = most;
-                parts[TILES * 16 * DIM + 2 * m + 1] = all;
-            } else if (q.lse) {
-                q.lse[line * (q.kv_heads * q.group) + h] = all == 0.0f ? -INFINITY : (most + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f;
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            if (i * 16 >= rows) break;
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kOut; ++e) *(f32x4*)(meet + (wave * 16 + n16) * kMergeRow + e * 16 + g * 4) = acc[i][e];
+            __syncthreads();
+            const int r = threadIdx.x / 16, m = i * 16 + r;
+            float most = refs[0][m];
+#pragma unroll
+            for (int w = 1; w < kAttendWaves; ++w) most = fmaxf(most, refs[w][m]);
+            float factor[kAttendWaves], all = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttendWaves; ++w) {
+                factor[w] = exp2_of(refs[w][m] - most);
+                all += factor[w] * sums[w][m];
             }
+            if (m >= rows) continue;
+#pragma unroll
+            for (int e = 0; e < DIM / 64; ++e) {
+                const int d = e * 64 + threadIdx.x % 16 * 4;
+                f32x4 x = {};
+#pragma unroll
+                for (int w = 0; w < kAttendWaves; ++w) x += factor[w] * *(const f32x4*)(meet + (w * 16 + r) * kMergeRow + d);
+                put(m, d, x, all);
+            }
+            if (threadIdx.x % 16 == 0) put_sum(m, most, all);
         }
     }
 }
 
 // Joins the splits of a row: a quarter of a wavefront to each row and head.
 template <int DIM>
-__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int tiles, int scaled)
+__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int rows, int scaled)
 {
     const int b = q.b0 + blockIdx.y;
     const Sequence s = sequence_within(q, b);
@@ -464,11 +532,11 @@ __global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int 
     const int heads = q.kv_heads * q.group;
     if (at >= s.count * heads) return;
     const int head = at / (s.count * q.group), full = at % (s.count * q.group);
-    const int block = full / (tiles * 16), m = full % (tiles * 16);
+    const int block = full / rows, m = full % rows;
     const int row = full / q.group, h = head * q.group + full % q.group;
-    const long long size = (long long)tiles * 16 * (DIM + 2);
+    const long long size = (long long)rows * (DIM + 2);
     const float* parts = q.parts + (((long long)b * q.kv_heads + head) * q.blocks + block) * q.splits * size;
-    const float* pairs = parts + (long long)tiles * 16 * DIM + 2 * m;
+    const float* pairs = parts + rows * DIM + 2 * m;
     float most = -INFINITY;
     for (int i = 0; i < reach.splits; ++i) most = fmaxf(most, pairs[i * size]);
     float all = 0.0f;
@@ -510,7 +578,7 @@ sv::AttendPlan plan_of(const spec_verify_attend_args* a)
     return sv::attend_plan(a->B, a->kv.kv_heads, padded_dim(a->kv.head_dim), (long long)a->rows * (a->heads / a->kv.kv_heads), most_seen(a));
 }
 
-template <int DIM, bool E4M3, int TILES>
+template <int DIM, bool E4M3, int TILES, bool SHARED>
 hipError_t launch_attend(const Attend& q, hipStream_t s)
 {
     constexpr int kMost = 0x7fffffff / kThreads; // workgroups of a launch, and more than enough
@@ -523,34 +591,36 @@ hipError_t launch_attend(const Attend& q, hipStream_t s)
         a.B = std::min(q.B - a.b0, step);
         long long groups = (long long)a.B * q.kv_heads * q.splits;
         if (q.blocks > 1) groups = (groups + 7) / 8 * 8 * q.blocks;
-        e = launch_kernel(sv_attend_kernel<DIM, E4M3, TILES>, dim3((unsigned)groups), dim3(kThreads), 0, s, nullptr, nullptr, a);
-        if (q.splits == 1) continue;
-        const dim3 grid(join, (unsigned)a.B);
-        if (e == hipSuccess)
-            e = launch_kernel(sv_attend_join_kernel<DIM>, grid, dim3(kThreads), 0, s, nullptr, nullptr, a, TILES, (int)(E4M3 && q.vscale));
+        e = launch_kernel(sv_attend_kernel<DIM, E4M3, TILES, SHARED>, dim3((unsigned)groups), dim3(kThreads), 0, s, nullptr, nullptr, a);
+        if (q.splits == 1 || e != hipSuccess) continue;
+        e = launch_kernel(sv_attend_join_kernel<DIM>, dim3(join, (unsigned)a.B), dim3(kThreads), 0, s, nullptr, nullptr, a,
+                          TILES * 16 * (SHARED ? kAttendWaves : 1), (int)(E4M3 && q.vscale));
     }
     return e;
 }
 
 template <int DIM, bool E4M3>
-hipError_t launch_tiles(const Attend& q, int tiles, hipStream_t s)
+hipError_t launch_tiles(const Attend& q, const sv::AttendPlan& p, hipStream_t s)
 {
-    switch (tiles) {
-    case 1: return launch_attend<DIM, E4M3, 1>(q, s);
-    case 2: return launch_attend<DIM, E4M3, 2>(q, s);
-    case 3: return launch_attend<DIM, E4M3, 3>(q, s);
+    if (!p.shared) {
+        if constexpr (DIM < 256)
+            if (p.tiles == 2) return launch_attend<DIM, E4M3, 2, false>(q, s);
+        return launch_attend<DIM, E4M3, 1, false>(q, s);
     }
-    if constexpr (DIM == 256) return launch_attend<DIM, E4M3, 4>(q, s);
-    else return tiles == 5 ? launch_attend<DIM, E4M3, 5>(q, s) : launch_attend<DIM, E4M3, 9>(q, s);
+    if constexpr (DIM < 256) {
+        if (p.tiles == 3) return launch_attend<DIM, E4M3, 3, true>(q, s);
+        if (p.tiles == 2) return launch_attend<DIM, E4M3, 2, true>(q, s);
+    }
+    return launch_attend<DIM, E4M3, 1, true>(q, s);
 }
 
 template <bool E4M3>
-hipError_t launch_dim(const Attend& q, int tiles, hipStream_t s)
+hipError_t launch_dim(const Attend& q, const sv::AttendPlan& p, hipStream_t s)
 {
     switch (padded_dim(q.dim)) {
-    case 64: return launch_tiles<64, E4M3>(q, tiles, s);
-    case 128: return launch_tiles<128, E4M3>(q, tiles, s);
-    default: return launch_tiles<256, E4M3>(q, tiles, s);
+    case 64: return launch_tiles<64, E4M3>(q, p, s);
+    case 128: return launch_tiles<128, E4M3>(q, p, s);
+    default: return launch_tiles<256, E4M3>(q, p, s);
     }
 }
 
@@ -582,7 +652,7 @@ int64_t spec_verify_attend_workspace_bytes(const spec_verify_config* cfg, const 
     if (a->B == 0) return 0;
     const sv::AttendPlan p = plan_of(a);
     if (p.splits == 1) return 0;
-    return (int64_t)a->B * a->kv.kv_heads * p.blocks * p.splits * p.tiles * 16 * (padded_dim(a->kv.head_dim) + 2) * 4;
+    return (int64_t)a->B * a->kv.kv_heads * p.blocks * p.splits * p.rows * (padded_dim(a->kv.head_dim) + 2) * 4;
 }
 
 int spec_verify_attend_check(const spec_verify_config* cfg, const spec_verify_attend_args* a)
@@ -647,7 +717,7 @@ int spec_verify_attend(spec_verify_t* h, const spec_verify_attend_args* a, void*
     q.span = p.span;
     q.parts = (float*)a->workspace;
     q.status = a->device_status;
-    e = e4m3 ? launch_dim<true>(q, p.tiles, s) : launch_dim<false>(q, p.tiles, s);
+    e = e4m3 ? launch_dim<true>(q, p, s) : launch_dim<false>(q, p, s);
     return e == hipSuccess ? SV_OK : SV_EDEVICE;
 }
 

@@ -188,13 +188,12 @@ int main()
             for (long long len : {0ll, 1ll, 127ll, 128ll, 129ll, 4000ll, 131000ll, 1ll << 30})
                 for (long long groups : {1ll, 3ll, 300ll, 5000ll, 1000000ll}) {
                     const sv::AttendPlan p = sv::attend_plan(groups, 1, dims[d], rows, len);
-                    if ((long long)p.blocks * p.tiles * 16 < rows || p.blocks < 1) return printf("rows %lld\\n", rows), 1;
+                    if ((long long)p.blocks * p.rows < rows || p.blocks < 1 || p.rows != p.tiles * (p.shared ? 64 : 16)) return printf("rows %lld\\n", rows), 1;
                     if ((long long)p.splits * p.span < len || p.splits < 1 || p.span % 128 || p.span < 128) return printf("len %lld\\n", len), 1;
-                    if (p.tiles > sv::attend_most_tiles(dims[d])) return printf("tiles %d\\n", p.tiles), 1;
-                    used[d][p.tiles] = true;
+                    used[d][p.tiles + 4 * p.shared] = true;
                 }
     for (int d = 0; d < 3; ++d) {
-        for (int t = 1; t < 10; ++t) if (used[d][t]) printf("%d ", t);
+        for (int t = 1; t < 10; ++t) if (used[d][t]) printf(t > 4 ? "s%d " : "%d ", t > 4 ? t - 4 : t);
         printf("| ");
     }
 }
@@ -204,4 +203,4 @@ int main()
                     str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
-    assert r.stdout.strip() == "1 2 3 5 9 | 1 2 3 5 9 | 1 2 3 4 |"
+    assert r.stdout.strip() == "1 2 s1 s2 s3 | 1 2 s1 s2 s3 | 1 s1 |"

@@ -60,9 +60,9 @@ struct Attend {
 // held back.
 __device__ __forceinline__ void wave_sync()
 {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
 // A barrier for LDS alone: loads from memory stay in flight.
@@ -141,27 +141,30 @@ __device__ __forceinline__ unsigned without_special(unsigned w)
 // each through its own part of LDS and with registers one tile ahead, without a barrier
 // until the end, where their sums are joined.
 // SHARED = true, for many rows: each wavefront has rows of its own and they share a tile
-// of 64 tokens in LDS, so that no sums are held twice.
+// of 64 tokens (32 of more than 128 columns) in LDS, so that no sums are held twice.
 template <int DIM, bool E4M3, int TILES, bool SHARED>
 __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 : DIM < 256 ? 2 : 1) void sv_attend_kernel(Attend q)
 {
     constexpr int kUnit = E4M3 ? 16 : 8;           // values of 16 bytes of the cache
     constexpr int kLanes = DIM / kUnit;            // lanes that read a token's row
-    constexpr int kTile = SHARED ? 2 * kAttendTokens : kAttendTokens; // tokens in LDS at a time
+    constexpr int kTile = SHARED && DIM < 256 ? 2 * kAttendTokens : kAttendTokens; // tokens in LDS at a time
     constexpr int kPer = (SHARED ? kThreads : 64) / kLanes; // tokens of a round of loads
     constexpr int kLoads = kTile / kPer;           // rounds of a tile, of keys and of values each
     constexpr int kSteps = DIM / 32;               // products of a score
     constexpr int kOut = DIM / 16;                 // tiles of a row of outputs
-    constexpr int kRows = TILES * 16 * (SHARED ? kAttendWaves : 1); // of the workgroup
+    constexpr int kTeams = SHARED ? kAttendWaves : 1; // wavefronts with rows of their own
+    constexpr int kRows = TILES * 16 * kTeams;     // of the workgroup
     constexpr int kTileBytes = kTile * DIM * 2;
     constexpr bool kTwo = SHARED;                  // keys and values in LDS of their own
-    constexpr bool kQueryLds = SHARED ? TILES > (DIM > 128 ? 0 : 1) : TILES > 1;
+    // tiles whose queries stay in registers; the others' are in LDS
+    constexpr int kQueryRegs = SHARED ? (DIM == 128 && TILES == 3 ? 1 : TILES) : TILES == 1 ? 1 : 0;
+    constexpr int kQueryLds = TILES - kQueryRegs;
     constexpr int kMergeRow = DIM + 4;             // floats of a row where the sums meet
     constexpr int kStage = SHARED ? 2 * kTileBytes : kAttendWaves * kTileBytes;
     constexpr int kMerge = SHARED ? 0 : kAttendWaves * 16 * kMergeRow * 4;
     constexpr int kStride = SHARED ? kTile : kTile * kAttendWaves;
     __shared__ __attribute__((aligned(16))) char stage[kStage > kMerge ? kStage : kMerge];
-    __shared__ u32x4 query[kQueryLds ? kRows / 16 * kSteps * 64 : 1];
+    __shared__ u32x4 query[kQueryLds ? kQueryLds * kTeams * kSteps * 64 : 1];
     __shared__ int place[kRows];                   // position of each row
     __shared__ unsigned noted[kRows * kOut];       // infinities beside the sums: bit 2i of column i, bit 2i + 1 the negative one; both: NaN
     __shared__ float refs[kAttendWaves][SHARED ? 1 : kRows], sums[kAttendWaves][SHARED ? 1 : kRows];
@@ -194,8 +197,9 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     const int rows = s.count * q.group - row0;     // and how many there are
     if (rows <= 0) return;
     const int first = reach.low + split * q.span, last = min(first + q.span, reach.end);
-    const int tile0 = SHARED ? wave * TILES : 0;   // first tile of the wavefront's rows
-    const int tiles = min(TILES, (rows + 15) / 16 - tile0); // and how many there are (SHARED: maybe none)
+    // tiles of the wavefront's rows (SHARED: every fourth), and how many there are
+    auto tile_of = [&](int i) { return SHARED ? i * kAttendWaves + wave : i; };
+    const int tiles = ((rows + 15) / 16 - (SHARED ? wave : 0) + kTeams - 1) / kTeams;
 
     // the queries, negative for a negative scale, as right operands; rows past the last
     // are those of the last
@@ -214,24 +218,21 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
         if (d < q.dim) x = *(const u32x4_any*)(from + d);
         return x ^ flip;
     };
-    u32x4 qreg[kQueryLds ? 1 : TILES][kQueryLds ? 1 : kSteps];
-    if constexpr (kQueryLds) {
-        for (int i = wave; i < kRows / 16 * kSteps; i += kAttendWaves) query[i * 64 + lane] = query_at(i / kSteps, i % kSteps);
-    } else {
+    u32x4 qreg[kQueryRegs ? kQueryRegs : 1][kSteps];
 #pragma unroll
-        for (int i = 0; i < TILES; ++i)
+    for (int i = 0; i < kQueryRegs; ++i)
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) qreg[i][k] = query_at(tile0 + i, k);
-    }
+        for (int k = 0; k < kSteps; ++k) qreg[i][k] = query_at(tile_of(i), k);
+    for (int i = wave; i < kQueryLds * kTeams * kSteps; i += kAttendWaves)
+        query[i * 64 + lane] = query_at(kQueryRegs * kTeams + i / kSteps, i % kSteps);
     for (int i = threadIdx.x; i < kRows * kOut; i += kThreads) noted[i] = 0;
     for (int i = threadIdx.x; i < kRows; i += kThreads) place[i] = s.start + (min(i, rows - 1) + row0) / q.group;
 
     // keys and values in LDS: a token's row of 16-byte chunks, their order changed from token
-    // to token so that a column of them lies in different banks
+    // to token so that a column of them, or a pair of columns, lies in different banks
     char* const kt = stage + (SHARED ? 0 : wave * kTileBytes);
     char* const vt = kTwo ? kt + kTileBytes : kt;
-    auto key_at = [](int t, int chunk) { return t * DIM * 2 + ((chunk ^ ((DIM == 64 ? t >> 1 : t) & (DIM < 128 ? 7 : 15))) * 16); };
-    auto value_at = [](int t, int half) { return t * DIM * 2 + ((half ^ ((DIM == 64 ? t >> 1 : t) & (DIM < 128 ? 3 : 7))) * 32); };
+    auto at = [](int t, int chunk) { return t * DIM * 2 + ((chunk ^ ((DIM == 64 ? t >> 1 : t) & (DIM < 128 ? 7 : 15))) * 16); };
     auto sync = [&] {
         if constexpr (SHARED) lds_barrier();
         else wave_sync();
@@ -242,7 +243,16 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     // which of a tile's tokens this lane loads in round 0, and which 16 bytes
     const int loader = SHARED ? threadIdx.x : lane;
     const bool lane_in = loader % kLanes * kUnit < q.dim;
-    const long long in_page = head * q.head_stride + (lane_in ? loader % kLanes * 16 : 0);
+    if (q.dim < DIM) { // columns past the head's size stay zero
+        for (int i = threadIdx.x; i < kStage / 16; i += kThreads) ((u32x4*)stage)[i] = u32x4{0, 0, 0, 0};
+        __syncthreads();
+    }
+    const char* const keys = q.keys + head * q.head_stride;
+    const char* const values = q.values + head * q.head_stride;
+    const unsigned in_row = lane_in ? loader % kLanes * 16 : 0;
+    // a wavefront's load is 64 / kLanes tokens in a row, in one page if that has as many places
+    const bool wide = (1 << q.c.shift) >= 64 / kLanes;
+    const unsigned in_group = lane / kLanes * q.token_stride + in_row;
 
     // the pages of a tile's tokens, a token to a lane; those past the end are the last
     auto pages_of = [&](int t0) { return table[min(t0 + (lane & (kTile - 1)), reach.end - 1) >> q.c.shift]; };
@@ -250,10 +260,19 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     auto is_bad = [&](int page) { return page < 0 || page >= q.c.n_pages; };
     auto load = [&](u32x4 (&x)[kLoads], const char* from, int t0, int page) { // of a bad page's tokens, the first page's
         if (is_bad(page)) page = 0;
+        if (wide) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int t = i * kPer + loader / kLanes;
-            x[i] = *(const u32x4*)(from + in_page + __shfl(page, t) * q.page_stride + (unsigned)(min(t0 + t, reach.end - 1) & mask) * (unsigned long long)q.token_stride);
+            for (int i = 0; i < kLoads; ++i) {
+                const int t = i * kPer + (SHARED ? wave * (64 / kLanes) : 0);
+                const char* group = from + __builtin_amdgcn_readlane(page, t) * q.page_stride + (long long)((t0 + t) & mask) * q.token_stride;
+                x[i] = *(const u32x4*)(group + in_group);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int t = i * kPer + loader / kLanes;
+                x[i] = *(const u32x4*)(from + __shfl(page, t) * q.page_stride + (unsigned)((t0 + t) & mask) * (unsigned long long)q.token_stride + in_row);
+            }
         }
     };
     auto widen = [](u32x4 x, int k) -> u32x4 { // eight values of a load as bf16
@@ -270,8 +289,8 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     int page = 0, next_page = 0; // of a token of the tile in hand and of the next
     if (t0 < last) {
         page = pages_of(t0);
-        load(kr, q.keys, t0, page);
-        load(vr, q.values, t0, page);
+        load(kr, keys, t0, page);
+        load(vr, values, t0, page);
         next_page = pages_of(t0 + kStride);
     }
     __syncthreads(); // queries and places
@@ -288,24 +307,25 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
         const bool mixed = t0 + kTile - 1 > s.start || gone || (q.window && t0 <= s.start + s.count - 1 - q.window);
         bool odd = false; // whether a value of a mixed tile is infinite or NaN
         auto store_keys = [&] {
+            if (lane_in)
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
+                for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-                for (int k = 0; k < kUnit / 8; ++k)
-                    *(u32x4*)(kt + key_at(i * kPer + in_load, unit * (kUnit / 8) + k)) = lane_in ? widen(kr[i], k) : u32x4{0, 0, 0, 0};
-            if (more) load(kr, q.keys, t0 + kStride, next_page);
+                    for (int k = 0; k < kUnit / 8; ++k)
+                        *(u32x4*)(kt + at(i * kPer + in_load, unit * (kUnit / 8) + k)) = widen(kr[i], k);
+            if (more) load(kr, keys, t0 + kStride, next_page);
         };
         auto store_values = [&] {
+            if (lane_in)
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
+                for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-                for (int k = 0; k < kUnit / 8; ++k) {
-                    const int chunk = unit * (kUnit / 8) + k;
-                    const u32x4 v = lane_in ? widen(vr[i], k) : u32x4{0, 0, 0, 0};
-                    if (mixed) odd |= special4(v);
-                    *(u32x4*)(vt + value_at(i * kPer + in_load, chunk / 2) + chunk % 2 * 16) = v;
-                }
-            if (more) load(vr, q.values, t0 + kStride, next_page);
+                    for (int k = 0; k < kUnit / 8; ++k) {
+                        const u32x4 v = widen(vr[i], k);
+                        if (mixed) odd |= special4(v);
+                        *(u32x4*)(vt + at(i * kPer + in_load, unit * (kUnit / 8) + k)) = v;
+                    }
+            if (more) load(vr, values, t0 + kStride, next_page);
         };
         // A weight of zero does not hide an infinity or a NaN from rows that do not see its
         // token.  Such values are noted for the rows that do, and taken as zero.
@@ -317,7 +337,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
                 const int t = t0 + in;
                 if (gone >> in & 1) continue;
                 for (int d = lane; d < q.dim; d += 64) {
-                    const unsigned x = *(const unsigned short*)(vt + value_at(in, d / 16) + d % 16 * 2);
+                    const unsigned x = *(const unsigned short*)(vt + at(in, d / 8) + d % 8 * 2);
                     if ((x & 0x7f80u) != 0x7f80u) continue;
                     const unsigned kind = (x & 0x7fu ? 3u : x & 0x8000u ? 2u : 1u) << (d % 16 * 2);
                     for (int m = 0; m < rows && m < kRows; ++m)
@@ -330,11 +350,11 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
 #pragma unroll
                 for (int k = 0; k < kUnit / 8; ++k) {
                     const int chunk = unit * (kUnit / 8) + k;
-                    u32x4* const at = (u32x4*)(vt + value_at(i * kPer + in_load, chunk / 2) + chunk % 2 * 16);
-                    u32x4 v = *at;
+                    u32x4* const here = (u32x4*)(vt + at(i * kPer + in_load, chunk));
+                    u32x4 v = *here;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = without_special(v[j]);
-                    *at = v;
+                    *here = v;
                 }
             sync();
         };
@@ -350,7 +370,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < kSteps; ++e) k[u][e] = *(const bf16x8*)(kt + key_at(in_tile + u * 16 + n16, e * 4 + g));
+                for (int e = 0; e < kSteps; ++e) k[u][e] = *(const bf16x8*)(kt + at(in_tile + u * 16 + n16, e * 4 + g));
             u32x4 p[TILES] = {};
 #pragma unroll
             for (int i = 0; i < TILES; ++i) {
@@ -358,21 +378,20 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
                 f32x4 x[2] = {};
 #pragma unroll
                 for (int e = 0; e < kSteps; ++e) {
-                    bf16x8 y;
-                    if constexpr (kQueryLds) y = __builtin_bit_cast(bf16x8, query[((tile0 + i) * kSteps + e) * 64 + lane_]);
-                    else y = __builtin_bit_cast(bf16x8, qreg[i][e]);
+                    const bf16x8 y = __builtin_bit_cast(bf16x8, i < kQueryRegs ? qreg[i < kQueryRegs ? i : 0][e]
+                                                                               : query[((tile_of(i) - kQueryRegs * kTeams) * kSteps + e) * 64 + lane_]);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][e], y, x[u], 0, 0, 0);
                 }
                 unsigned hidden = 0; // bit u * 4 + j
                 if (mixed) {
-                    const int at = place[(tile0 + i) * 16 + n16], low = q.window ? at - q.window : -1;
+                    const int here = place[tile_of(i) * 16 + n16], low = q.window ? here - q.window : -1;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int in = in_tile + u * 16 + g * 4 + j, t = t0 + in;
-                            if (t > at || t <= low || (gone >> in & 1)) {
+                            if (t > here || t <= low || (gone >> in & 1)) {
                                 hidden |= 1u << (u * 4 + j);
                                 x[u][j] = -FLT_MAX;
                             }
@@ -420,7 +439,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int t = in_tile + u * 16 + g * 4 + n16 / 4;
-                    v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + value_at(t, e) + n16 % 4 * 8));
+                    v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + at(t, 2 * e + n16 % 4 / 2) + n16 % 2 * 8));
                 }
                 const u32x2 lo = __builtin_bit_cast(u32x2, v[0]), hi = __builtin_bit_cast(u32x2, v[1]);
                 const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
@@ -475,7 +494,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     if constexpr (SHARED) {
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
-            const int m = (tile0 + i) * 16 + n16;
+            const int m = tile_of(i) * 16 + n16;
             if (m >= rows) continue;
 #pragma unroll
             for (int e = 0; e < kOut; ++e) put(m, e * 16 + g * 4, acc[i][e], sum[i]);
@@ -519,45 +538,61 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     }
 }
 
-// Joins the splits of a row: a quarter of a wavefront to each row and head.
+// Joins the splits of a row and head: DIM / 4 lanes hold its columns, `parts` such
+// groups take every parts-th split and meet in LDS.
 template <int DIM>
-__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int rows, int scaled)
+__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int rows, int parts)
 {
+    constexpr int kLanes = DIM / 4;
+    __shared__ f32x4 meet[kThreads];
+    __shared__ float refs[kThreads / kLanes], sums[kThreads / kLanes];
     const int b = q.b0 + blockIdx.y;
     const Sequence s = sequence_within(q, b);
     if (s.count <= 0) return;
     const Reach reach = reach_of(q, s);
     if (reach.splits <= 1) return;
-    const int at = blockIdx.x * 16 + threadIdx.x / 16; // row of the sequence, over all heads
-    const int heads = q.kv_heads * q.group;
-    if (at >= s.count * heads) return;
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes, part = group % parts;
+    const int heads = q.kv_heads * q.group, total = s.count * heads;
+    const int each = kThreads / kLanes / parts; // rows of a workgroup
+    if ((int)blockIdx.x * each >= total) return;
+    const int at = min((int)blockIdx.x * each + group / parts, total - 1); // row of the sequence, over all heads
     const int head = at / (s.count * q.group), full = at % (s.count * q.group);
     const int block = full / rows, m = full % rows;
-    const int row = full / q.group, h = head * q.group + full % q.group;
     const long long size = (long long)rows * (DIM + 2);
-    const float* parts = q.parts + (((long long)b * q.kv_heads + head) * q.blocks + block) * q.splits * size;
-    const float* pairs = parts + rows * DIM + 2 * m;
-    float most = -INFINITY;
-    for (int i = 0; i < reach.splits; ++i) most = fmaxf(most, pairs[i * size]);
-    float all = 0.0f;
-    constexpr int kEach = DIM / 64;
-    f32x4 x[kEach] = {};
-    for (int i = 0; i < reach.splits; ++i) {
+    const float* from = q.parts + (((long long)b * q.kv_heads + head) * q.blocks + block) * q.splits * size;
+    const float* pairs = from + rows * DIM + 2 * m;
+    float most = -FLT_MAX, all = 0.0f;
+#pragma unroll 4
+    for (int i = part; i < reach.splits; i += parts) most = fmaxf(most, pairs[i * size]);
+    f32x4 x = {};
+#pragma unroll 4
+    for (int i = part; i < reach.splits; i += parts) {
         const float factor = exp2_of(pairs[i * size] - most);
         all += factor * pairs[i * size + 1];
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) x[e] += factor * *(const f32x4*)(parts + i * size + m * DIM + e * 64 + threadIdx.x % 16 * 4);
+        x += factor * *(const f32x4*)(from + i * size + m * DIM + lane * 4);
     }
-    const float by = all == 0.0f ? 0.0f : (scaled ? q.vscale[head] : 1.0f) / all;
+    if (parts > 1) {
+        meet[threadIdx.x] = x;
+        if (lane == 0) refs[group] = most, sums[group] = all;
+        __syncthreads();
+        const int first = group - part;
+        for (int i = 0; i < parts; ++i) most = fmaxf(most, refs[first + i]);
+        x = f32x4{};
+        all = 0.0f;
+        for (int i = 0; i < parts; ++i) {
+            const float factor = exp2_of(refs[first + i] - most);
+            all += factor * sums[first + i];
+            x += factor * meet[(first + i) * kLanes + lane];
+        }
+        if (part) return;
+    }
+    if ((int)blockIdx.x * each + group / parts >= total) return;
+    const int row = full / q.group, h = head * q.group + full % q.group, d = lane * 4;
+    const float by = all == 0.0f ? 0.0f : (q.vscale ? q.vscale[head] : 1.0f) / all;
     const long long line = q.r.roff ? s.first + row : (long long)b * q.r.rows + row;
-    unsigned short* to = q.out + (q.r.roff ? line * q.orow : b * q.ob + row * q.orow) + h * q.oh;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        const int d = e * 64 + threadIdx.x % 16 * 4;
-        if (d < q.dim) *(u32x2_any*)(to + d) = u32x2{pack_bf16(x[e][0] * by, x[e][1] * by), pack_bf16(x[e][2] * by, x[e][3] * by)};
-    }
-    if (q.lse && threadIdx.x % 16 == 0)
-        q.lse[line * heads + h] = all == 0.0f ? -INFINITY : (most + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f;
+    unsigned short* to = q.out + (q.r.roff ? line * q.orow : b * q.ob + row * q.orow) + h * q.oh + d;
+    if (d < q.dim) *(u32x2_any*)to = u32x2{pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by)};
+    if (q.lse && lane == 0) q.lse[line * heads + h] = all == 0.0f ? -INFINITY : (most + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f;
 }
 
 __global__ void sv_attend_status_kernel(int* status) { *status = 0; }
@@ -582,7 +617,10 @@ template <int DIM, bool E4M3, int TILES, bool SHARED>
 hipError_t launch_attend(const Attend& q, hipStream_t s)
 {
     constexpr int kMost = 0x7fffffff / kThreads; // workgroups of a launch, and more than enough
-    const unsigned join = (unsigned)(((long long)q.r.rows * q.kv_heads * q.group + 15) / 16);
+    int parts = 1; // groups that join a row: half as many as it has splits
+    while (parts * 2 <= kThreads / (DIM / 4) && parts * 2 < q.splits) parts *= 2;
+    const int each = kThreads / (DIM / 4) / parts;
+    const unsigned join = (unsigned)(((long long)q.r.rows * q.kv_heads * q.group + each - 1) / each);
     const long long per = std::max<long long>((long long)q.kv_heads * q.blocks * q.splits, join);
     const int step = (int)std::max(1ll, std::min<long long>(65535, (kMost - 8 * q.blocks) / per));
     hipError_t e = hipSuccess;
@@ -594,7 +632,7 @@ hipError_t launch_attend(const Attend& q, hipStream_t s)
         e = launch_kernel(sv_attend_kernel<DIM, E4M3, TILES, SHARED>, dim3((unsigned)groups), dim3(kThreads), 0, s, nullptr, nullptr, a);
         if (q.splits == 1 || e != hipSuccess) continue;
         e = launch_kernel(sv_attend_join_kernel<DIM>, dim3(join, (unsigned)a.B), dim3(kThreads), 0, s, nullptr, nullptr, a,
-                          TILES * 16 * (SHARED ? kAttendWaves : 1), (int)(E4M3 && q.vscale));
+                          TILES * 16 * (SHARED ? kAttendWaves : 1), parts);
     }
     return e;
 }
@@ -663,7 +701,7 @@ int spec_verify_attend_check(const spec_verify_config* cfg, const spec_verify_at
     if (rc == SV_OK) rc = sv::check_rows(cfg, a->B, a->cache, a->slots, a->last_row, a->row_offsets);
     if (rc != SV_OK) return rc;
     if (!(fabsf(a->scale) <= FLT_MAX)) return SV_EINVAL;
-    if (a->kv.token_stride > (1 << 28)) return SV_EUNSUPPORTED;
+    if (a->kv.token_stride > (1 << 26)) return SV_EUNSUPPORTED; // 16 tokens of 2 bytes within 32 bits
     if (a->B == 0) return SV_OK;
     if (!a->queries || !a->outputs) return SV_EINVAL;
     const int dim = a->kv.head_dim;
@@ -707,8 +745,8 @@ int spec_verify_attend(spec_verify_t* h, const spec_verify_attend_args* a, void*
     q.page_stride = a->kv.page_stride * es;
     q.head_stride = a->kv.head_stride * es;
     q.token_stride = (unsigned)(a->kv.token_stride * es);
-    q.kscale = a->kv.key_scales;
-    q.vscale = a->kv.value_scales;
+    q.kscale = e4m3 ? a->kv.key_scales : nullptr;
+    q.vscale = e4m3 ? a->kv.value_scales : nullptr;
     q.scale = a->scale;
     q.window = a->window;
     q.max_len = a->max_len ? a->max_len : a->cache.max_pages * a->cache.page_size;

@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "spec_verify.h"
 #include "sv_attend_plan.h"
@@ -14,7 +15,10 @@
 using sv::cache_status;
 using sv::cache_uniform;
 using sv::DeviceGuard;
+using sv::kAttendBatch;
+using sv::kAttendBegin;
 using sv::kAttendTokens;
+using sv::kAttendUnit;
 using sv::kAttendWaves;
 using sv::launch_kernel;
 using sv::Sequence;
@@ -22,6 +26,13 @@ using sv::Sequence;
 namespace {
 
 constexpr int kThreads = 64 * kAttendWaves;
+// Wavefronts to a SIMD that the registers are shared out for.
+constexpr int attend_waves(int dim, bool e4m3, int tiles, bool shared)
+{
+    return shared ? 2 : dim == 64 ? (tiles == 1 ? 3 : 2) : e4m3 ? 2 : dim == 128 && tiles < 3 ? 2 : 1;
+}
+
+constexpr float kRoom = 16.0f; // how far (in log2) a score may lie above its row's reference
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -50,8 +61,9 @@ struct Attend {
     const float* vscale;
     float scale;
     int window, max_len;
-    int blocks, splits, span;
-    float* parts;               // [B][kv_heads][blocks][splits]: sums of a workgroup, then its (reference, sum) pairs
+    int blocks, shares;
+    int* ends;                  // [B]: where each sequence's units end among all of the launch; null: none is split
+    float* parts;               // [shares][kv_heads][blocks][2]: sums of a workgroup, then its (reference, sum) pairs
     int* status;
 };
 
@@ -73,10 +85,9 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// The tokens that a sequence's rows see, and how they are split.
+// The tokens that a sequence's rows see.
 struct Reach {
     int low, end; // low: a multiple of the tile
-    int splits;
 };
 
 __device__ __forceinline__ Reach reach_of(const Attend& q, const Sequence& s)
@@ -85,16 +96,29 @@ __device__ __forceinline__ Reach reach_of(const Attend& q, const Sequence& s)
     r.end = s.start + s.count;
     r.low = 0;
     if (q.window && s.start + 1 > q.window) r.low = (s.start + 1 - q.window) / kAttendTokens * kAttendTokens;
-    r.splits = (r.end - r.low + q.span - 1) / q.span;
     return r;
 }
 
 // The sequence, with those marked bad that are longer than the caller said.
+template <bool UNIFORM = true>
 __device__ __forceinline__ Sequence sequence_within(const Attend& q, int b)
 {
-    Sequence s = sv::sequence_of(q.c, q.r, b);
+    Sequence s = sv::sequence_of<UNIFORM>(q.c, q.r, b);
     if (s.count > 0 && s.start + s.count > q.max_len) s.count = -1;
     return s;
+}
+
+// All sequences' units of tokens, one after the other, are cut into equal shares.  A
+// sequence counts kAttendBegin units more than it has, in front.  These are the units
+// from .. to - 1 of a sequence that ends at `end`, after one that ends at `base`, in a
+// share from lo to hi - 1 (from >= to: none).
+struct Piece {
+    int from, to;
+};
+
+__device__ __forceinline__ Piece piece_of(int base, int end, int lo, int hi)
+{
+    return Piece{max(0, max(lo, base) - base - kAttendBegin), max(0, min(hi, end) - base - kAttendBegin)};
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -128,7 +152,17 @@ __device__ __forceinline__ unsigned without_special(unsigned w)
     return w;
 }
 
-// Attention of one block of rows over one split of a sequence's length.
+// The kernel's arguments, in memory: the compiler does not know that they are the same at
+// every call.
+__device__ __forceinline__ const Attend* fresh_args()
+{
+    typedef const __attribute__((address_space(4))) char* Kernarg;
+    Kernarg p = (Kernarg)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return (const Attend*)p;
+}
+
+// Attention of a block of rows over a share of the sequences' tokens.
 //
 // The scores of a tile of 16 tokens and 16 rows are K Q^T, so that a lane holds one
 // row's scores of four tokens in each of two tiles; rounded, these are in place as
@@ -143,7 +177,7 @@ __device__ __forceinline__ unsigned without_special(unsigned w)
 // SHARED = true, for many rows: each wavefront has rows of its own and they share a tile
 // of 64 tokens (32 of more than 128 columns) in LDS, so that no sums are held twice.
 template <int DIM, bool E4M3, int TILES, bool SHARED>
-__global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 : DIM < 256 ? 2 : 1) void sv_attend_kernel(Attend q)
+__global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) void sv_attend_kernel(Attend args)
 {
     constexpr int kUnit = E4M3 ? 16 : 8;           // values of 16 bytes of the cache
     constexpr int kLanes = DIM / kUnit;            // lanes that read a token's row
@@ -161,45 +195,95 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     constexpr int kQueryLds = TILES - kQueryRegs;
     constexpr int kMergeRow = DIM + 4;             // floats of a row where the sums meet
     constexpr int kStage = SHARED ? 2 * kTileBytes : kAttendWaves * kTileBytes;
-    constexpr int kMerge = SHARED ? 0 : kAttendWaves * 16 * kMergeRow * 4;
+    constexpr int kMerge = kAttendWaves * 16 * kMergeRow * 4;
     constexpr int kStride = SHARED ? kTile : kTile * kAttendWaves;
     __shared__ __attribute__((aligned(16))) char stage[kStage > kMerge ? kStage : kMerge];
     __shared__ u32x4 query[kQueryLds ? kQueryLds * kTeams * kSteps * 64 : 1];
     __shared__ int place[kRows];                   // position of each row
     __shared__ unsigned noted[kRows * kOut];       // infinities beside the sums: bit 2i of column i, bit 2i + 1 the negative one; both: NaN
-    __shared__ float refs[kAttendWaves][SHARED ? 1 : kRows], sums[kAttendWaves][SHARED ? 1 : kRows];
+    __shared__ float refs[kAttendWaves][16], sums[kAttendWaves][16];
+    __shared__ int ends[kAttendBatch];
 
-    const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // consecutive workgroups go round the eight dies; the row blocks that read the same
-    // tokens follow each other on one
-    unsigned id = blockIdx.x;
-    int block = 0;
-    if (q.blocks > 1) {
-        const unsigned die = id % 8, turn = id / 8;
-        block = (int)(turn % q.blocks);
-        id = turn / q.blocks * 8 + die;
-    }
-    const unsigned per = (unsigned)q.kv_heads * q.B;
-    const int split = (int)(id / per);
-    if (split >= q.splits) return;
-    const unsigned in_split = id % per;
-    const int b = q.b0 + (int)(in_split / q.kv_heads), head = (int)(in_split % q.kv_heads);
+    // Consecutive workgroups go round the eight dies.  What reads the same tokens, or tokens
+    // beside each other (row blocks, and key-value heads in one page), follows on one die.
+    unsigned id = blockIdx.x / 8;
+    const int block = (int)(id % args.blocks);
+    id /= args.blocks;
+    const int head = (int)(id % args.kv_heads);
+    const int share = (int)(id / args.kv_heads * 8 + blockIdx.x % 8);
+    if (share >= args.shares) return;
 
-    const Sequence s = sequence_within(q, b);
-    if (s.count <= 0) {
-        if (s.count < 0 && threadIdx.x == 0) cache_status(q.status, SV_STATUS_BAD_INPUT);
-        return;
+    // where each sequence's units end
+    {
+        const int each = (args.B + kThreads - 1) / kThreads, b0 = threadIdx.x * each;
+        int count[kAttendBatch / kThreads], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kAttendBatch / kThreads; ++i) {
+            count[i] = 0;
+            if (i >= each || b0 + i >= args.B) continue;
+            const Sequence s = sequence_within<false>(args, args.b0 + b0 + i);
+            if (s.count < 0 && blockIdx.x == 0) cache_status(args.status, SV_STATUS_BAD_INPUT);
+            if (s.count <= 0) continue;
+            const Reach reach = reach_of(args, s);
+            count[i] = (reach.end - reach.low + kAttendUnit - 1) / kAttendUnit + kAttendBegin;
+            sum += count[i];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int y = __shfl_up(upto, d);
+            if (lane >= d) upto += y;
+        }
+        if (lane == 63) place[wave] = upto;
+        __syncthreads();
+        upto -= sum;
+        for (int w = 0; w < wave; ++w) upto += place[w];
+#pragma unroll
+        for (int i = 0; i < kAttendBatch / kThreads; ++i) {
+            if (i >= each || b0 + i >= args.B) continue;
+            upto += count[i];
+            ends[b0 + i] = upto;
+            if (args.ends && blockIdx.x == 0) args.ends[args.b0 + b0 + i] = upto;
+        }
+        __syncthreads();
     }
+    const int total = ends[args.B - 1], width = (total + args.shares - 1) / args.shares;
+    const int lo = share * width, hi = min(total, lo + width);
+    int next = 0; // the first sequence that ends behind lo
+    for (int n = args.B; n > 0;) {
+        const int half = n / 2;
+        if (ends[next + half] <= lo) next += half + 1, n -= half + 1;
+        else n = half;
+    }
+    for (; next < args.B; ++next) {
+    // What a piece needs is worked out anew for it: kept from piece to piece, it would take
+    // the registers that the sums need.
+    const Attend& q = *fresh_args();
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int n16 = lane & 15, g = lane >> 4;
+    const int base = next ? __builtin_amdgcn_readfirstlane(ends[next - 1]) : 0, end = __builtin_amdgcn_readfirstlane(ends[next]);
+    if (base >= hi) break;
+    const Piece piece = piece_of(base, end, lo, hi);
+    if (piece.from >= piece.to) continue;
+    const int b = q.b0 + next;
+    const Sequence s = sequence_within(q, b);
+    if (s.count <= 0) continue;
     const Reach reach = reach_of(q, s);
-    if (split >= reach.splits) return;
     const int row0 = block * kRows;                // first row (of a row and a head) of the workgroup
     const int rows = s.count * q.group - row0;     // and how many there are
-    if (rows <= 0) return;
-    const int first = reach.low + split * q.span, last = min(first + q.span, reach.end);
-    // tiles of the wavefront's rows (SHARED: every fourth), and how many there are
-    auto tile_of = [&](int i) { return SHARED ? i * kAttendWaves + wave : i; };
-    const int tiles = ((rows + 15) / 16 - (SHARED ? wave : 0) + kTeams - 1) / kTeams;
+    if (rows <= 0) continue;
+    const int first = reach.low + piece.from * kAttendUnit, last = min(reach.low + piece.to * kAttendUnit, reach.end);
+    __syncthreads(); // the piece before has left LDS
+    // Tiles of rows.  SHARED: each wavefront has every fourth tile of as many as go round; one
+    // tile that is left over is taken by all four in turn, 32 tokens each, two by two wavefronts
+    // each, three by one each, as their last tile.  What is taken in turn is summed at the end.
+    const int all_tiles = min(TILES * kTeams, (rows + 15) / 16);
+    const int full = all_tiles / kTeams, left = all_tiles % kTeams;
+    const int takers = left == 1 ? 4 : left == 2 ? 2 : 1;     // of a tile that is left over
+    auto tile_of = [&](int i) { return SHARED ? (left && i == TILES - 1 ? full * kTeams + wave / takers : i * kTeams + wave) : i; };
 
     // the queries, negative for a negative scale, as right operands; rows past the last
     // are those of the last
@@ -207,8 +291,6 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     if (E4M3 && q.kscale) scale *= cache_uniform(q.kscale + head);
     const unsigned flip = scale < 0 ? 0x80008000u : 0u;
     scale = fabsf(scale);
-    const float room = 16.0f / scale;              // how far a score may lie above its reference
-    const bool followed = room < FLT_MAX;          // (a scale of about zero: the reference is 0)
     auto query_at = [&](int tile, int step) {
         const int m = min(tile * 16 + n16, rows - 1) + row0;
         const int r = m / q.group, h = head * q.group + m % q.group;
@@ -223,16 +305,19 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     for (int i = 0; i < kQueryRegs; ++i)
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) qreg[i][k] = query_at(tile_of(i), k);
-    for (int i = wave; i < kQueryLds * kTeams * kSteps; i += kAttendWaves)
-        query[i * 64 + lane] = query_at(kQueryRegs * kTeams + i / kSteps, i % kSteps);
+    for (int i = SHARED ? wave : 0; i < kQueryLds * kTeams * kSteps; i += kTeams) // (not SHARED: all write the same)
+        query[i * 64 + lane] = query_at(tile_of(kQueryRegs + i / (kTeams * kSteps)), i / kTeams % kSteps);
     for (int i = threadIdx.x; i < kRows * kOut; i += kThreads) noted[i] = 0;
     for (int i = threadIdx.x; i < kRows; i += kThreads) place[i] = s.start + (min(i, rows - 1) + row0) / q.group;
 
     // keys and values in LDS: a token's row of 16-byte chunks, their order changed from token
-    // to token so that a column of them, or a pair of columns, lies in different banks
+    // to token so that a column of 16 of them, and a pair of columns of 8, lie in different banks
     char* const kt = stage + (SHARED ? 0 : wave * kTileBytes);
     char* const vt = kTwo ? kt + kTileBytes : kt;
-    auto at = [](int t, int chunk) { return t * DIM * 2 + ((chunk ^ ((DIM == 64 ? t >> 1 : t) & (DIM < 128 ? 7 : 15))) * 16); };
+    auto turn_of = [](int t) { return ((DIM == 64 ? (t >> 1 & 3) * 2 : (t & 7) * 2) + (t >> 3 & 1)) * 16; };
+    auto at = [&](int t, int chunk) { return t * DIM * 2 + ((chunk * 16) ^ turn_of(t)); };
+    // the same for a place that is known (token t, bits of a chunk) away from a lane's own
+    auto off = [&](int base, int t, int chunk) { return t * DIM * 2 + (base ^ (chunk * 16 ^ turn_of(t))); };
     auto sync = [&] {
         if constexpr (SHARED) lds_barrier();
         else wave_sync();
@@ -249,6 +334,9 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     }
     const char* const keys = q.keys + head * q.head_stride;
     const char* const values = q.values + head * q.head_stride;
+    // a lane's own places in LDS: where it writes, its first key and its first value
+    const int write_at = at(loader / kLanes, loader % kLanes * (kUnit / 8));
+    const int key_at = at(n16, g), value_at = at(g * 4 + n16 / 4, n16 % 4 / 2) + n16 % 2 * 8;
     const unsigned in_row = lane_in ? loader % kLanes * 16 : 0;
     // a wavefront's load is 64 / kLanes tokens in a row, in one page if that has as many places
     const bool wide = (1 << q.c.shift) >= 64 / kLanes;
@@ -281,9 +369,9 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     };
 
     f32x4 acc[TILES][kOut] = {};
-    float ref[TILES], top[TILES], sum[TILES]; // ref: a score; top = ref * scale
+    float top[TILES], sum[TILES]; // top: a row's reference, a scaled score
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) ref[i] = followed ? -FLT_MAX : 0.0f, top[i] = followed ? -FLT_MAX : 0.0f, sum[i] = 0.0f;
+    for (int i = 0; i < TILES; ++i) top[i] = -FLT_MAX, sum[i] = 0.0f;
 
     int t0 = first + (SHARED ? 0 : wave * kTile);
     int page = 0, next_page = 0; // of a token of the tile in hand and of the next
@@ -296,11 +384,9 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
     __syncthreads(); // queries and places
     for (; t0 < last; t0 += kStride) {
         const bool more = t0 + kStride < last;
-        // with many sums to hold, places in LDS are worked out anew rather than kept
-        int lane_ = lane;
-        if constexpr (TILES > 1) asm volatile("" : "+v"(lane_));
-        const int n16 = lane_ & 15, g = lane_ >> 4;
-        const int loader = SHARED ? wave * 64 + lane_ : lane_, in_load = loader / kLanes, unit = loader % kLanes;
+        // asked for ahead of the next tile's keys and values, so that it is there when they are
+        const int far_page = pages_of(t0 + 2 * kStride);
+        __builtin_amdgcn_sched_barrier(0);
         const unsigned long long gone = __ballot(is_bad(page)); // tokens whose page is bad
         if (gone && lane == 0) cache_status(q.status, SV_STATUS_BAD_INPUT);
         // some row does not see some token
@@ -312,7 +398,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
                 for (int i = 0; i < kLoads; ++i)
 #pragma unroll
                     for (int k = 0; k < kUnit / 8; ++k)
-                        *(u32x4*)(kt + at(i * kPer + in_load, unit * (kUnit / 8) + k)) = widen(kr[i], k);
+                        *(u32x4*)(kt + off(write_at, i * kPer, k)) = widen(kr[i], k);
             if (more) load(kr, keys, t0 + kStride, next_page);
         };
         auto store_values = [&] {
@@ -323,7 +409,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
                     for (int k = 0; k < kUnit / 8; ++k) {
                         const u32x4 v = widen(vr[i], k);
                         if (mixed) odd |= special4(v);
-                        *(u32x4*)(vt + at(i * kPer + in_load, unit * (kUnit / 8) + k)) = v;
+                        *(u32x4*)(vt + off(write_at, i * kPer, k)) = v;
                     }
             if (more) load(vr, values, t0 + kStride, next_page);
         };
@@ -349,8 +435,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
             for (int i = 0; i < kLoads; ++i)
 #pragma unroll
                 for (int k = 0; k < kUnit / 8; ++k) {
-                    const int chunk = unit * (kUnit / 8) + k;
-                    u32x4* const here = (u32x4*)(vt + at(i * kPer + in_load, chunk));
+                    u32x4* const here = (u32x4*)(vt + off(write_at, i * kPer, k));
                     u32x4 v = *here;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = without_special(v[j]);
@@ -366,97 +451,108 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
         for (int part = 0; part < kTile / kAttendTokens; ++part) { // 32 tokens at a time
             if (part && t0 + part * kAttendTokens >= last) break;
             const int in_tile = part * kAttendTokens;
-            bf16x8 k[2][kSteps];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < kSteps; ++e) k[u][e] = *(const bf16x8*)(kt + at(in_tile + u * 16 + n16, e * 4 + g));
-            u32x4 p[TILES] = {};
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                if (SHARED && i >= tiles) break;
-                f32x4 x[2] = {};
+            // whether these tokens count for the wavefront's last tile
+            const bool last_too = !SHARED ? full == TILES : left ? wave < left * takers && (t0 - first + in_tile) / kAttendTokens % takers == wave % takers : full == TILES;
+            u32x4 p[TILES] = {}; // weights
+            // the weights of tiles from .. to - 1 of the wavefront
+            auto score = [&](auto from, auto to) {
+                f32x4 x[to - from][2] = {};
 #pragma unroll
                 for (int e = 0; e < kSteps; ++e) {
-                    const bf16x8 y = __builtin_bit_cast(bf16x8, i < kQueryRegs ? qreg[i < kQueryRegs ? i : 0][e]
-                                                                               : query[((tile_of(i) - kQueryRegs * kTeams) * kSteps + e) * 64 + lane_]);
+                    bf16x8 k[2];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][e], y, x[u], 0, 0, 0);
+                    for (int u = 0; u < 2; ++u) k[u] = *(const bf16x8*)(kt + off(key_at, in_tile + u * 16, e * 4));
+#pragma unroll
+                    for (int i = from; i < to; ++i) {
+                        const bf16x8 y = __builtin_bit_cast(bf16x8, i < kQueryRegs ? qreg[i < kQueryRegs ? i : 0][e]
+                                                                                   : query[(((i - kQueryRegs) * kSteps + e) * kTeams + (SHARED ? wave : 0)) * 64 + lane]);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) x[i - from][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u], y, x[i - from][u], 0, 0, 0);
+                    }
                 }
-                unsigned hidden = 0; // bit u * 4 + j
-                if (mixed) {
-                    const int here = place[tile_of(i) * 16 + n16], low = q.window ? here - q.window : -1;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                for (int i = from; i < to; ++i) {
+                    if (i < TILES - 1 && i >= full) continue;
+                    const f32x4* const y = x[i - from];
+                    // w: how far the scores lie above the reference; those that are not seen at -infinity
+                    float w[8], most;
+                    auto above = [&] {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int in = in_tile + u * 16 + g * 4 + j, t = t0 + in;
-                            if (t > here || t <= low || (gone >> in & 1)) {
-                                hidden |= 1u << (u * 4 + j);
-                                x[u][j] = -FLT_MAX;
+                        for (int j = 0; j < 8; ++j) w[j] = fmaf(y[j / 4][j % 4], scale, -top[i]);
+                        if (mixed) {
+                            const int here = place[tile_of(i) * 16 + n16], low = q.window ? here - q.window : -1;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int in = in_tile + j / 4 * 16 + g * 4 + j % 4, t = t0 + in;
+                                if ((t > here) | (t <= low) | (int)(gone >> in & 1)) w[j] = -INFINITY;
                             }
                         }
-                }
-                if (followed) {
-                    float most = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
-                    if (__ballot(most > ref[i] + room)) {
+                        most = fmaxf(fmaxf(fmaxf(fmaxf(w[0], w[1]), w[2]), fmaxf(fmaxf(w[3], w[4]), w[5])), fmaxf(w[6], w[7]));
+                    };
+                    above();
+                    if (__ballot(most > kRoom)) {
+                        most = -FLT_MAX;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) most = fmaxf(most, w[j] == -INFINITY ? -FLT_MAX : y[j / 4][j % 4] * scale);
                         most = fmaxf(most, __shfl_xor(most, 16));
                         most = fmaxf(most, __shfl_xor(most, 32));
-                        most = fmaxf(most, ref[i]);
+                        most = fmaxf(most, top[i]);
                         // (every lane takes part: sums that only some lanes change would be held twice)
-                        const float now = most > ref[i] ? most * scale : top[i], factor = exp2_of(top[i] - now);
-                        ref[i] = most;
-                        top[i] = now;
+                        const float factor = exp2_of(top[i] - most);
+                        top[i] = most;
                         sum[i] *= factor;
 #pragma unroll
                         for (int e = 0; e < kOut; ++e) acc[i][e] *= factor;
+                        above();
                     }
-                }
-                float w[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = exp2_of(fmaf(x[j / 4][j % 4], scale, -top[i]));
-                if (mixed) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (hidden >> j & 1) w[j] = 0.0f;
+                    for (int j = 0; j < 8; ++j) w[j] = exp2_of(w[j]);
+                    sum[i] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+                    // rounded to bf16, as the matrix cores take them: half a step of 2^-8 each, as the
+                    // outputs' own rounding is
+                    p[i] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
                 }
-                sum[i] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-                // rounded to bf16, as the matrix cores take them: half a step of 2^-8 each, as the
-                // outputs' own rounding is
-                p[i] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
-                if constexpr (TILES > 1) __builtin_amdgcn_sched_barrier(0); // one tile after the other, or their scores pile up and spill
-            }
-            if constexpr (!kTwo) {
+            };
+            auto weigh = [&](auto from, auto to) { // out^T += V^T P^T
+#pragma unroll
+                for (int e = 0; e < kOut; ++e) {
+                    s16x4 v[2]; // values of four tokens of each half, a column to each lane: tokens u * 16 + g * 4 + j
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + off(value_at, in_tile + u * 16, 2 * e)));
+                    const u32x2 lo = __builtin_bit_cast(u32x2, v[0]), hi = __builtin_bit_cast(u32x2, v[1]);
+                    const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+#pragma unroll
+                    for (int i = from; i < to; ++i)
+                        acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, p[i]), acc[i][e], 0, 0, 0);
+                }
+            };
+            constexpr std::integral_constant<int, 0> kFirst;
+            constexpr std::integral_constant<int, TILES - 1> kLast;
+            constexpr std::integral_constant<int, TILES> kEnd;
+            if constexpr (SHARED) {
+                if (TILES > 1 && full) {
+                    if constexpr (TILES > 1) score(kFirst, kLast), weigh(kFirst, kLast);
+                }
+                // (left out where another wavefront takes it: weights of zero would make NaN of an infinity)
+                if (last_too) score(kLast, kEnd), weigh(kLast, kEnd);
+            } else {
+                score(kFirst, kEnd);
                 sync(); // the keys are read
                 store_values();
                 sync();
                 if (mixed) take_out();
-            }
-#pragma unroll
-            for (int e = 0; e < kOut; ++e) {
-                // values of four tokens of each half, a column to each lane: tokens u * 16 + g * 4 + j
-                s16x4 v[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = in_tile + u * 16 + g * 4 + n16 / 4;
-                    v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + at(t, 2 * e + n16 % 4 / 2) + n16 % 2 * 8));
-                }
-                const u32x2 lo = __builtin_bit_cast(u32x2, v[0]), hi = __builtin_bit_cast(u32x2, v[1]);
-                const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
-#pragma unroll
-                for (int i = 0; i < TILES; ++i)
-                    acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, p[i]), acc[i][e], 0, 0, 0);
+                weigh(kFirst, kEnd);
             }
         }
         sync(); // the tile is read
         page = next_page;
-        if (more) next_page = pages_of(t0 + 2 * kStride);
+        next_page = far_page;
     }
 
     const float vscale = E4M3 && q.vscale ? cache_uniform(q.vscale + head) : 1.0f;
-    const bool whole = reach.splits == 1;
-    float* const parts = q.parts + (((long long)b * q.kv_heads + head) * q.blocks + block) * ((long long)q.splits * (kRows * (DIM + 2)))
-                       + (long long)split * (kRows * (DIM + 2));
+    const bool whole = piece.from == 0 && last == reach.end;
+    float* const parts = q.parts + ((((long long)share * q.kv_heads + head) * q.blocks + block) * 2 + (base > lo)) * (kRows * (DIM + 2));
     // stores four columns of row m of the workgroup, with what was noted for them
     auto put = [&](int m, int d, f32x4 x, float all) {
         const unsigned also = noted[m * kOut + d / 16] >> (d % 16 * 2) & 0xffu;
@@ -491,66 +587,80 @@ __global__ __launch_bounds__(kThreads, SHARED ? 2 : DIM == 64 && TILES == 1 ? 4 
         sum[i] += __shfl_xor(sum[i], 16);
         sum[i] += __shfl_xor(sum[i], 32);
     }
+    // Where wavefronts have sums of the same rows, they meet in LDS: `takers` of them, from
+    // wavefront `from` on, brought the same tile of the rows.
+    float* const meet = (float*)stage;
+    auto join = [&](int tile, int from, int takers) {
+        const int r = threadIdx.x / 16, m = tile * 16 + r;
+        float most = -FLT_MAX, all = 0.0f, factor[kAttendWaves];
+#pragma unroll
+        for (int w = 0; w < kAttendWaves; ++w)
+            if (w < takers) most = fmaxf(most, refs[from + w][r]);
+#pragma unroll
+        for (int w = 0; w < kAttendWaves; ++w) {
+            factor[w] = w < takers ? exp2_of(refs[from + w][r] - most) : 0.0f;
+            if (w < takers) all += factor[w] * sums[from + w][r];
+        }
+        if (m >= rows) return;
+#pragma unroll
+        for (int e = 0; e < DIM / 64; ++e) {
+            const int d = e * 64 + threadIdx.x % 16 * 4;
+            f32x4 x = {};
+#pragma unroll
+            for (int w = 0; w < kAttendWaves; ++w)
+                if (w < takers) x += factor[w] * *(const f32x4*)(meet + ((from + w) * 16 + r) * kMergeRow + d);
+            put(m, d, x, all);
+        }
+        if (threadIdx.x % 16 == 0) put_sum(m, most, all);
+    };
+    // puts tile i of every wavefront there
+    auto bring = [&](int i) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) *(f32x4*)(meet + (wave * 16 + n16) * kMergeRow + e * 16 + g * 4) = acc[i][e];
+        if (g == 0) refs[wave][n16] = top[i], sums[wave][n16] = sum[i];
+        __syncthreads();
+    };
     if constexpr (SHARED) {
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
             const int m = tile_of(i) * 16 + n16;
-            if (m >= rows) continue;
+            if (i >= full || m >= rows) continue;
 #pragma unroll
             for (int e = 0; e < kOut; ++e) put(m, e * 16 + g * 4, acc[i][e], sum[i]);
             if (g == 0) put_sum(m, top[i], sum[i]);
         }
-    } else {
-        // the four wavefronts' sums, a tile of rows at a time
-        float* const meet = (float*)stage;
-        if (g == 0) {
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) refs[wave][i * 16 + n16] = top[i], sums[wave][i * 16 + n16] = sum[i];
+        if (left) {
+            bring(TILES - 1);
+            for (int k = 0; k < left; ++k) join(full * kTeams + k, k * takers, takers);
         }
+    } else {
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
             if (i * 16 >= rows) break;
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < kOut; ++e) *(f32x4*)(meet + (wave * 16 + n16) * kMergeRow + e * 16 + g * 4) = acc[i][e];
-            __syncthreads();
-            const int r = threadIdx.x / 16, m = i * 16 + r;
-            float most = refs[0][m];
-#pragma unroll
-            for (int w = 1; w < kAttendWaves; ++w) most = fmaxf(most, refs[w][m]);
-            float factor[kAttendWaves], all = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kAttendWaves; ++w) {
-                factor[w] = exp2_of(refs[w][m] - most);
-                all += factor[w] * sums[w][m];
-            }
-            if (m >= rows) continue;
-#pragma unroll
-            for (int e = 0; e < DIM / 64; ++e) {
-                const int d = e * 64 + threadIdx.x % 16 * 4;
-                f32x4 x = {};
-#pragma unroll
-                for (int w = 0; w < kAttendWaves; ++w) x += factor[w] * *(const f32x4*)(meet + (w * 16 + r) * kMergeRow + d);
-                put(m, d, x, all);
-            }
-            if (threadIdx.x % 16 == 0) put_sum(m, most, all);
+            bring(i);
+            join(i, 0, kAttendWaves);
         }
+    }
     }
 }
 
-// Joins the splits of a row and head: DIM / 4 lanes hold its columns, `parts` such
-// groups take every parts-th split and meet in LDS.
+// Joins the pieces of a row and head: DIM / 4 lanes hold its columns, `parts` such
+// groups take every parts-th piece and meet in LDS.
 template <int DIM>
-__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int rows, int parts)
+__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int b1, int rows, int parts)
 {
     constexpr int kLanes = DIM / 4;
     __shared__ f32x4 meet[kThreads];
     __shared__ float refs[kThreads / kLanes], sums[kThreads / kLanes];
-    const int b = q.b0 + blockIdx.y;
+    const int b = q.b0 + b1 + blockIdx.y;
+    const int base = b > q.b0 ? cache_uniform(q.ends + b - 1) : 0, end = cache_uniform(q.ends + b);
+    const int width = (cache_uniform(q.ends + q.b0 + q.B - 1) + q.shares - 1) / q.shares;
+    if (base == end) return;
+    const int first = (base + kAttendBegin) / width, last = (end - 1) / width; // shares that have some of it
+    if (first == last) return;
     const Sequence s = sequence_within(q, b);
     if (s.count <= 0) return;
-    const Reach reach = reach_of(q, s);
-    if (reach.splits <= 1) return;
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes, part = group % parts;
     const int heads = q.kv_heads * q.group, total = s.count * heads;
     const int each = kThreads / kLanes / parts; // rows of a workgroup
@@ -558,31 +668,33 @@ __global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int 
     const int at = min((int)blockIdx.x * each + group / parts, total - 1); // row of the sequence, over all heads
     const int head = at / (s.count * q.group), full = at % (s.count * q.group);
     const int block = full / rows, m = full % rows;
-    const long long size = (long long)rows * (DIM + 2);
-    const float* from = q.parts + (((long long)b * q.kv_heads + head) * q.blocks + block) * q.splits * size;
-    const float* pairs = from + rows * DIM + 2 * m;
+    const long long size = (long long)rows * (DIM + 2), step = size * 2 * q.blocks * q.kv_heads;
+    const float* from = q.parts + ((long long)head * q.blocks + block) * 2 * size;
+    // (only the share in which the sequence begins may have it in second place)
+    auto sums_of = [&](int share) { return from + share * step + (base > share * width ? size : 0); };
     float most = -FLT_MAX, all = 0.0f;
 #pragma unroll 4
-    for (int i = part; i < reach.splits; i += parts) most = fmaxf(most, pairs[i * size]);
+    for (int i = first + part; i <= last; i += parts) most = fmaxf(most, sums_of(i)[rows * DIM + 2 * m]);
     f32x4 x = {};
 #pragma unroll 4
-    for (int i = part; i < reach.splits; i += parts) {
-        const float factor = exp2_of(pairs[i * size] - most);
-        all += factor * pairs[i * size + 1];
-        x += factor * *(const f32x4*)(from + i * size + m * DIM + lane * 4);
+    for (int i = first + part; i <= last; i += parts) {
+        const float* of = sums_of(i);
+        const float factor = exp2_of(of[rows * DIM + 2 * m] - most);
+        all += factor * of[rows * DIM + 2 * m + 1];
+        x += factor * *(const f32x4*)(of + m * DIM + lane * 4);
     }
     if (parts > 1) {
         meet[threadIdx.x] = x;
         if (lane == 0) refs[group] = most, sums[group] = all;
         __syncthreads();
-        const int first = group - part;
-        for (int i = 0; i < parts; ++i) most = fmaxf(most, refs[first + i]);
+        const int group0 = group - part;
+        for (int i = 0; i < parts; ++i) most = fmaxf(most, refs[group0 + i]);
         x = f32x4{};
         all = 0.0f;
         for (int i = 0; i < parts; ++i) {
-            const float factor = exp2_of(refs[first + i] - most);
-            all += factor * sums[first + i];
-            x += factor * meet[(first + i) * kLanes + lane];
+            const float factor = exp2_of(refs[group0 + i] - most);
+            all += factor * sums[group0 + i];
+            x += factor * meet[(group0 + i) * kLanes + lane];
         }
         if (part) return;
     }
@@ -610,29 +722,27 @@ long long most_seen(const spec_verify_attend_args* a)
 
 sv::AttendPlan plan_of(const spec_verify_attend_args* a)
 {
-    return sv::attend_plan(a->B, a->kv.kv_heads, padded_dim(a->kv.head_dim), (long long)a->rows * (a->heads / a->kv.kv_heads), most_seen(a));
+    return sv::attend_plan(a->B, a->kv.kv_heads, padded_dim(a->kv.head_dim), a->kv.type == SV_KV_E4M3, (long long)a->rows * (a->heads / a->kv.kv_heads), most_seen(a));
 }
 
 template <int DIM, bool E4M3, int TILES, bool SHARED>
-hipError_t launch_attend(const Attend& q, hipStream_t s)
+hipError_t launch_attend(const Attend& q, int batch, hipStream_t s)
 {
-    constexpr int kMost = 0x7fffffff / kThreads; // workgroups of a launch, and more than enough
-    int parts = 1; // groups that join a row: half as many as it has splits
-    while (parts * 2 <= kThreads / (DIM / 4) && parts * 2 < q.splits) parts *= 2;
+    const long long groups = (long long)(q.shares + 7) / 8 * 8 * q.kv_heads * q.blocks; // (at most 1024 * 1024 * 86 * 8 / 8)
+    int parts = 1; // groups that join a row: half as many as it may have pieces
+    while (parts * 2 <= kThreads / (DIM / 4) && parts * 2 < q.shares) parts *= 2;
     const int each = kThreads / (DIM / 4) / parts;
     const unsigned join = (unsigned)(((long long)q.r.rows * q.kv_heads * q.group + each - 1) / each);
-    const long long per = std::max<long long>((long long)q.kv_heads * q.blocks * q.splits, join);
-    const int step = (int)std::max(1ll, std::min<long long>(65535, (kMost - 8 * q.blocks) / per));
     hipError_t e = hipSuccess;
     Attend a = q;
-    for (a.b0 = 0; a.b0 < q.B && e == hipSuccess; a.b0 += step) {
-        a.B = std::min(q.B - a.b0, step);
-        long long groups = (long long)a.B * q.kv_heads * q.splits;
-        if (q.blocks > 1) groups = (groups + 7) / 8 * 8 * q.blocks;
+    for (a.b0 = 0; a.b0 < q.B && e == hipSuccess; a.b0 += batch) {
+        a.B = std::min(q.B - a.b0, batch);
         e = launch_kernel(sv_attend_kernel<DIM, E4M3, TILES, SHARED>, dim3((unsigned)groups), dim3(kThreads), 0, s, nullptr, nullptr, a);
-        if (q.splits == 1 || e != hipSuccess) continue;
-        e = launch_kernel(sv_attend_join_kernel<DIM>, dim3(join, (unsigned)a.B), dim3(kThreads), 0, s, nullptr, nullptr, a,
-                          TILES * 16 * (SHARED ? kAttendWaves : 1), parts);
+        if (!q.ends || e != hipSuccess) continue;
+        const int most = (int)std::max(1ll, std::min<long long>(65535, 0xffffffffll / kThreads / join)); // of a launch
+        for (int b1 = 0; b1 < a.B && e == hipSuccess; b1 += most)
+            e = launch_kernel(sv_attend_join_kernel<DIM>, dim3(join, (unsigned)std::min(a.B - b1, most)), dim3(kThreads), 0, s, nullptr, nullptr,
+                              a, b1, TILES * 16 * (SHARED ? kAttendWaves : 1), parts);
     }
     return e;
 }
@@ -640,16 +750,11 @@ hipError_t launch_attend(const Attend& q, hipStream_t s)
 template <int DIM, bool E4M3>
 hipError_t launch_tiles(const Attend& q, const sv::AttendPlan& p, hipStream_t s)
 {
-    if (!p.shared) {
-        if constexpr (DIM < 256)
-            if (p.tiles == 2) return launch_attend<DIM, E4M3, 2, false>(q, s);
-        return launch_attend<DIM, E4M3, 1, false>(q, s);
-    }
     if constexpr (DIM < 256) {
-        if (p.tiles == 3) return launch_attend<DIM, E4M3, 3, true>(q, s);
-        if (p.tiles == 2) return launch_attend<DIM, E4M3, 2, true>(q, s);
+        if (p.tiles == 3) return p.shared ? launch_attend<DIM, E4M3, 3, true>(q, p.batch, s) : launch_attend<DIM, E4M3, 3, false>(q, p.batch, s);
+        if (p.tiles == 2) return p.shared ? launch_attend<DIM, E4M3, 2, true>(q, p.batch, s) : launch_attend<DIM, E4M3, 2, false>(q, p.batch, s);
     }
-    return launch_attend<DIM, E4M3, 1, true>(q, s);
+    return p.shared ? launch_attend<DIM, E4M3, 1, true>(q, p.batch, s) : launch_attend<DIM, E4M3, 1, false>(q, p.batch, s);
 }
 
 template <bool E4M3>
@@ -660,6 +765,15 @@ hipError_t launch_dim(const Attend& q, const sv::AttendPlan& p, hipStream_t s)
     case 128: return launch_tiles<128, E4M3>(q, p, s);
     default: return launch_tiles<256, E4M3>(q, p, s);
     }
+}
+
+// Whether a sequence may be too long for one unit.
+bool may_split(const spec_verify_attend_args* a) { return most_seen(a) > kAttendUnit; }
+
+// Workspace for the pieces of sequences that are split; behind it, where each ends.
+int64_t parts_bytes(const spec_verify_attend_args* a, const sv::AttendPlan& p)
+{
+    return (int64_t)p.shares * a->kv.kv_heads * p.blocks * 2 * p.rows * (padded_dim(a->kv.head_dim) + 2) * 4;
 }
 
 // All that does not look at the buffers of the rows and the workspace.
@@ -689,8 +803,8 @@ int64_t spec_verify_attend_workspace_bytes(const spec_verify_config* cfg, const 
     if (rc != SV_OK) return rc;
     if (a->B == 0) return 0;
     const sv::AttendPlan p = plan_of(a);
-    if (p.splits == 1) return 0;
-    return (int64_t)a->B * a->kv.kv_heads * p.blocks * p.splits * p.rows * (padded_dim(a->kv.head_dim) + 2) * 4;
+    if (!may_split(a)) return 0;
+    return parts_bytes(a, p) + ((int64_t)a->B * 4 + 15) / 16 * 16;
 }
 
 int spec_verify_attend_check(const spec_verify_config* cfg, const spec_verify_attend_args* a)
@@ -751,9 +865,9 @@ int spec_verify_attend(spec_verify_t* h, const spec_verify_attend_args* a, void*
     q.window = a->window;
     q.max_len = a->max_len ? a->max_len : a->cache.max_pages * a->cache.page_size;
     q.blocks = p.blocks;
-    q.splits = p.splits;
-    q.span = p.span;
+    q.shares = p.shares;
     q.parts = (float*)a->workspace;
+    q.ends = may_split(a) ? (int*)((char*)a->workspace + parts_bytes(a, p)) : nullptr;
     q.status = a->device_status;
     e = e4m3 ? launch_dim<true>(q, p, s) : launch_dim<false>(q, p, s);
     return e == hipSuccess ? SV_OK : SV_EDEVICE;

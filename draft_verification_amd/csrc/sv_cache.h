@@ -46,10 +46,16 @@ struct Sequence {
     long long first;
 };
 
+// (UNIFORM: every lane asks for the same b)
+template <bool UNIFORM = true>
 __device__ __forceinline__ Sequence sequence_of(const Cache& c, const Rows& q, int b)
 {
+    auto get = [](const auto* p) {
+        if constexpr (UNIFORM) return cache_uniform(p);
+        else return *p;
+    };
     Sequence s;
-    s.slot = q.slots ? cache_uniform(q.slots + b) : b;
+    s.slot = q.slots ? get(q.slots + b) : b;
     s.count = -1;
     s.start = 0;
     s.first = 0;
@@ -60,12 +66,12 @@ __device__ __forceinline__ Sequence sequence_of(const Cache& c, const Rows& q, i
     if (s.slot < 0 || s.slot >= c.n_slots) return s;
     int n = q.rows;
     if (q.roff) {
-        s.first = cache_uniform(q.roff + b);
-        const long long end = cache_uniform(q.roff + b + 1);
+        s.first = get(q.roff + b);
+        const long long end = get(q.roff + b + 1);
         if (s.first < 0 || end < s.first || end - s.first > q.rows) return s;
         n = (int)(end - s.first);
     } else if (q.last_row) {
-        const int last = cache_uniform(q.last_row + b);
+        const int last = get(q.last_row + b);
         if (last < -1) return s;
         if (last < n) n = last + 1;
     }
@@ -73,8 +79,8 @@ __device__ __forceinline__ Sequence sequence_of(const Cache& c, const Rows& q, i
         s.count = 0;
         return s;
     }
-    const int len = cache_uniform(c.lengths + s.slot);
-    const int held = c.counts ? min(cache_uniform(c.counts + s.slot), c.max_pages) : c.max_pages;
+    const int len = get(c.lengths + s.slot);
+    const int held = c.counts ? min(get(c.counts + s.slot), c.max_pages) : c.max_pages;
     if (len < 0 || (long long)len + q.row0 + n > ((long long)held << c.shift)) return s;
     s.start = len + q.row0;
     s.count = n;

@@ -185,13 +185,17 @@ int main()
     bool used[3][10] = {};
     for (int d = 0; d < 3; ++d)
         for (long long rows = 1; rows < 17000; rows += rows < 400 ? 1 : 37)
-            for (long long len : {0ll, 1ll, 127ll, 128ll, 129ll, 4000ll, 131000ll, 1ll << 30})
-                for (long long groups : {1ll, 3ll, 300ll, 5000ll, 1000000ll}) {
-                    const sv::AttendPlan p = sv::attend_plan(groups, 1, dims[d], rows, len);
-                    if ((long long)p.blocks * p.rows < rows || p.blocks < 1 || p.rows != p.tiles * (p.shared ? 64 : 16)) return printf("rows %lld\\n", rows), 1;
-                    if ((long long)p.splits * p.span < len || p.splits < 1 || p.span % 128 || p.span < 128) return printf("len %lld\\n", len), 1;
-                    used[d][p.tiles + 4 * p.shared] = true;
-                }
+            for (long long len : {1ll, 127ll, 128ll, 129ll, 4000ll, 131000ll, 1ll << 30})
+                for (long long B : {1ll, 3ll, 300ll, 5000ll, 1000000ll})
+                    for (int kv : {1, 5, 16, 1024}) {
+                        const sv::AttendPlan p = sv::attend_plan(B, kv, dims[d], rows % 2, rows, len);
+                        if ((long long)p.blocks * p.rows < rows || p.blocks < 1 || p.rows != p.tiles * (p.shared ? 64 : 16)) return printf("rows %lld\\n", rows), 1;
+                        if (p.batch < 1 || p.batch > B || p.batch > 1024 || p.shares < 8 || p.shares % 8) return printf("B %lld\\n", B), 1;
+                        // the units of a launch, and what is rounded up, stay within 32 bits, and so do its work-items
+                        if (p.batch * (sv::attend_units(len) + sv::kAttendBegin) + p.shares > 0x7fffffffll) return printf("len %lld\\n", len), 1;
+                        if ((long long)p.shares * kv * p.blocks * 256 > 0xffffffffll) return printf("groups %d %d %d\\n", p.shares, kv, p.blocks), 1;
+                        used[d][p.tiles + 4 * p.shared] = true;
+                    }
     for (int d = 0; d < 3; ++d) {
         for (int t = 1; t < 10; ++t) if (used[d][t]) printf(t > 4 ? "s%d " : "%d ", t > 4 ? t - 4 : t);
         printf("| ");
@@ -203,4 +207,4 @@ int main()
                     str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
-    assert r.stdout.strip() == "1 2 s1 s2 s3 | 1 2 s1 s2 s3 | 1 s1 |"
+    assert r.stdout.strip() == "1 2 3 s1 s2 s3 | 1 2 3 s1 s2 s3 | 1 s1 |"

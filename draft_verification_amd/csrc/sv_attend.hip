@@ -26,6 +26,7 @@ using sv::Sequence;
 namespace {
 
 constexpr int kThreads = 64 * kAttendWaves;
+
 // Wavefronts to a SIMD that the registers are shared out for.
 constexpr int attend_waves(int dim, bool e4m3, int tiles, bool shared)
 {
@@ -63,6 +64,7 @@ struct Attend {
     int window, max_len;
     int blocks, shares;
     int* ends;                  // [B]: where each sequence's units end among all of the launch; null: none is split
+    int* starts;                // [shares]: the sequence in which each share begins
     float* parts;               // [shares][kv_heads][blocks][2]: sums of a workgroup, then its (reference, sum) pairs
     int* status;
 };
@@ -77,7 +79,7 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// A barrier for LDS alone: loads from memory stay in flight.
+// A barrier for LDS alone: what is under way from and to memory stays so.
 __device__ __forceinline__ void lds_barrier()
 {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -190,6 +192,9 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     constexpr int kRows = TILES * 16 * kTeams;     // of the workgroup
     constexpr int kTileBytes = kTile * DIM * 2;
     constexpr bool kTwo = SHARED;                  // keys and values in LDS of their own
+    // Keys and values take turns in registers, each half a tile ahead, rather than both being one
+    // tile ahead.
+    constexpr bool kHalves = !SHARED && !E4M3;
     // tiles whose queries stay in registers; the others' are in LDS
     constexpr int kQueryRegs = SHARED ? (DIM == 128 && TILES == 3 ? 1 : TILES) : TILES == 1 ? 1 : 0;
     constexpr int kQueryLds = TILES - kQueryRegs;
@@ -203,6 +208,8 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     __shared__ unsigned noted[kRows * kOut];       // infinities beside the sums: bit 2i of column i, bit 2i + 1 the negative one; both: NaN
     __shared__ float refs[kAttendWaves][16], sums[kAttendWaves][16];
     __shared__ int ends[kAttendBatch];
+    __shared__ Sequence known[kAttendBatch];
+    static_assert(kAttendBatch == kThreads, "a thread to each sequence");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -215,20 +222,17 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     const int share = (int)(id / args.kv_heads * 8 + blockIdx.x % 8);
     if (share >= args.shares) return;
 
-    // where each sequence's units end
+    // what each sequence has, and where its units end; a thread to each
     {
-        const int each = (args.B + kThreads - 1) / kThreads, b0 = threadIdx.x * each;
-        int count[kAttendBatch / kThreads], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kAttendBatch / kThreads; ++i) {
-            count[i] = 0;
-            if (i >= each || b0 + i >= args.B) continue;
-            const Sequence s = sequence_within<false>(args, args.b0 + b0 + i);
+        int sum = 0;
+        if ((int)threadIdx.x < args.B) {
+            const Sequence s = sequence_within<false>(args, args.b0 + threadIdx.x);
             if (s.count < 0 && blockIdx.x == 0) cache_status(args.status, SV_STATUS_BAD_INPUT);
-            if (s.count <= 0) continue;
-            const Reach reach = reach_of(args, s);
-            count[i] = (reach.end - reach.low + kAttendUnit - 1) / kAttendUnit + kAttendBegin;
-            sum += count[i];
+            if (s.count > 0) {
+                const Reach reach = reach_of(args, s);
+                sum = (reach.end - reach.low + kAttendUnit - 1) / kAttendUnit + kAttendBegin;
+            }
+            known[threadIdx.x] = s;
         }
         int upto = sum;
 #pragma unroll
@@ -237,17 +241,11 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
             if (lane >= d) upto += y;
         }
         if (lane == 63) place[wave] = upto;
-        __syncthreads();
-        upto -= sum;
+        lds_barrier();
         for (int w = 0; w < wave; ++w) upto += place[w];
-#pragma unroll
-        for (int i = 0; i < kAttendBatch / kThreads; ++i) {
-            if (i >= each || b0 + i >= args.B) continue;
-            upto += count[i];
-            ends[b0 + i] = upto;
-            if (args.ends && blockIdx.x == 0) args.ends[args.b0 + b0 + i] = upto;
-        }
-        __syncthreads();
+        ends[threadIdx.x] = upto;
+        if (args.ends && blockIdx.x == 0 && (int)threadIdx.x < args.B) args.ends[threadIdx.x] = upto;
+        lds_barrier();
     }
     const int total = ends[args.B - 1], width = (total + args.shares - 1) / args.shares;
     const int lo = share * width, hi = min(total, lo + width);
@@ -257,6 +255,7 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
         if (ends[next + half] <= lo) next += half + 1, n -= half + 1;
         else n = half;
     }
+    if (args.ends && head == 0 && block == 0 && threadIdx.x == 0) args.starts[share] = next;
     for (; next < args.B; ++next) {
     // What a piece needs is worked out anew for it: kept from piece to piece, it would take
     // the registers that the sums need.
@@ -269,14 +268,17 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     const Piece piece = piece_of(base, end, lo, hi);
     if (piece.from >= piece.to) continue;
     const int b = q.b0 + next;
-    const Sequence s = sequence_within(q, b);
-    if (s.count <= 0) continue;
+    Sequence s;
+    s.slot = __builtin_amdgcn_readfirstlane(known[next].slot);
+    s.count = __builtin_amdgcn_readfirstlane(known[next].count);
+    s.start = __builtin_amdgcn_readfirstlane(known[next].start);
+    s.first = known[next].first;
     const Reach reach = reach_of(q, s);
     const int row0 = block * kRows;                // first row (of a row and a head) of the workgroup
     const int rows = s.count * q.group - row0;     // and how many there are
     if (rows <= 0) continue;
     const int first = reach.low + piece.from * kAttendUnit, last = min(reach.low + piece.to * kAttendUnit, reach.end);
-    __syncthreads(); // the piece before has left LDS
+    lds_barrier(); // the piece before has left LDS
     // Tiles of rows.  SHARED: each wavefront has every fourth tile of as many as go round; one
     // tile that is left over is taken by all four in turn, 32 tokens each, two by two wavefronts
     // each, three by one each, as their last tile.  What is taken in turn is summed at the end.
@@ -291,24 +293,11 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     if (E4M3 && q.kscale) scale *= cache_uniform(q.kscale + head);
     const unsigned flip = scale < 0 ? 0x80008000u : 0u;
     scale = fabsf(scale);
-    auto query_at = [&](int tile, int step) {
-        const int m = min(tile * 16 + n16, rows - 1) + row0;
-        const int r = m / q.group, h = head * q.group + m % q.group;
-        const unsigned short* from = q.q + (q.r.roff ? (s.first + r) * q.qr : b * q.qb + r * q.qr) + h * q.qh;
-        const int d = step * 32 + g * 8;
-        u32x4 x = {0, 0, 0, 0};
-        if (d < q.dim) x = *(const u32x4_any*)(from + d);
-        return x ^ flip;
-    };
-    u32x4 qreg[kQueryRegs ? kQueryRegs : 1][kSteps];
-#pragma unroll
-    for (int i = 0; i < kQueryRegs; ++i)
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) qreg[i][k] = query_at(tile_of(i), k);
-    for (int i = SHARED ? wave : 0; i < kQueryLds * kTeams * kSteps; i += kTeams) // (not SHARED: all write the same)
-        query[i * 64 + lane] = query_at(tile_of(kQueryRegs + i / (kTeams * kSteps)), i / kTeams % kSteps);
+    // m / group, exactly: m + 0.5 lies at least 1 / 128 from a multiple, and m below 2^15
+    const float by_group = 1.0f / q.group;
+    auto row_of = [&](int m) { return (int)((m + 0.5f) * by_group); };
     for (int i = threadIdx.x; i < kRows * kOut; i += kThreads) noted[i] = 0;
-    for (int i = threadIdx.x; i < kRows; i += kThreads) place[i] = s.start + (min(i, rows - 1) + row0) / q.group;
+    for (int i = threadIdx.x; i < kRows; i += kThreads) place[i] = s.start + row_of(min(i, rows - 1) + row0);
 
     // keys and values in LDS: a token's row of 16-byte chunks, their order changed from token
     // to token so that a column of 16 of them, and a pair of columns of 8, lie in different banks
@@ -330,13 +319,13 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     const bool lane_in = loader % kLanes * kUnit < q.dim;
     if (q.dim < DIM) { // columns past the head's size stay zero
         for (int i = threadIdx.x; i < kStage / 16; i += kThreads) ((u32x4*)stage)[i] = u32x4{0, 0, 0, 0};
-        __syncthreads();
+        lds_barrier();
     }
     const char* const keys = q.keys + head * q.head_stride;
     const char* const values = q.values + head * q.head_stride;
     // a lane's own places in LDS: where it writes, its first key and its first value
-    const int write_at = at(loader / kLanes, loader % kLanes * (kUnit / 8));
-    const int key_at = at(n16, g), value_at = at(g * 4 + n16 / 4, n16 % 4 / 2) + n16 % 2 * 8;
+    const int write_at0 = at(loader / kLanes, loader % kLanes * (kUnit / 8));
+    const int key_at0 = at(n16, g), value_at0 = at(g * 4 + n16 / 4, n16 % 4 / 2) + n16 % 2 * 8;
     const unsigned in_row = lane_in ? loader % kLanes * 16 : 0;
     // a wavefront's load is 64 / kLanes tokens in a row, in one page if that has as many places
     const bool wide = (1 << q.c.shift) >= 64 / kLanes;
@@ -373,17 +362,54 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
 #pragma unroll
     for (int i = 0; i < TILES; ++i) top[i] = -FLT_MAX, sum[i] = 0.0f;
 
+    // What is asked for from memory comes behind all that other workgroups of the compute unit
+    // have asked for: as few steps as can be.  First the pages of two tiles and the queries, ...
     int t0 = first + (SHARED ? 0 : wave * kTile);
-    int page = 0, next_page = 0; // of a token of the tile in hand and of the next
-    if (t0 < last) {
-        page = pages_of(t0);
-        load(kr, keys, t0, page);
-        load(vr, values, t0, page);
-        next_page = pages_of(t0 + kStride);
+    int page = pages_of(t0), next_page = pages_of(t0 + kStride); // of a token of the tile in hand and of the next
+    auto query_at = [&](int tile, int step) {
+        const int m = min(tile * 16 + n16, rows - 1) + row0;
+        const int r = row_of(m), h = head * q.group + m - r * q.group;
+        const unsigned short* from = q.q + (q.r.roff ? (s.first + r) * q.qr : b * q.qb + r * q.qr) + h * q.qh;
+        const int d = step * 32 + g * 8;
+        u32x4 x = {0, 0, 0, 0};
+        if (d < q.dim) x = *(const u32x4_any*)(from + d);
+        return x;
+    };
+    u32x4 qreg[kQueryRegs ? kQueryRegs : 1][kSteps];
+#pragma unroll
+    for (int i = 0; i < kQueryRegs; ++i)
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) qreg[i][k] = query_at(tile_of(i), k);
+    // (a wavefront's own where rows are split, and else a share of all)
+    constexpr int kQueryEach = SHARED ? kQueryLds * kSteps : (kQueryLds * kSteps + kAttendWaves - 1) / kAttendWaves;
+    u32x4 qlds[kQueryEach ? kQueryEach : 1];
+#pragma unroll
+    for (int i = 0; i < kQueryEach; ++i) {
+        const int k = SHARED ? i : min(i * kAttendWaves + wave, kQueryLds * kSteps - 1);
+        qlds[i] = query_at(tile_of(kQueryRegs + k / kSteps), k % kSteps);
     }
-    __syncthreads(); // queries and places
+    // ... then keys and values
+    __builtin_amdgcn_sched_barrier(0);
+    if (t0 < last) {
+        load(kr, keys, t0, page);
+        if constexpr (!kHalves) load(vr, values, t0, page);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kQueryRegs; ++i)
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) qreg[i][k] ^= flip;
+#pragma unroll
+    for (int i = 0; i < kQueryEach; ++i) {
+        const int k = SHARED ? i * kTeams + wave : min(i * kAttendWaves + wave, kQueryLds * kSteps - 1);
+        query[k * 64 + lane] = qlds[i] ^ flip;
+    }
+    lds_barrier(); // queries and places
     for (; t0 < last; t0 += kStride) {
         const bool more = t0 + kStride < last;
+        // with many sums to hold, places in LDS are worked out anew rather than kept
+        int key_at = key_at0, value_at = value_at0, write_at = write_at0;
+        if constexpr (TILES > 1 || DIM == 256) asm volatile("" : "+v"(key_at), "+v"(value_at), "+v"(write_at));
         // asked for ahead of the next tile's keys and values, so that it is there when they are
         const int far_page = pages_of(t0 + 2 * kStride);
         __builtin_amdgcn_sched_barrier(0);
@@ -399,7 +425,8 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
 #pragma unroll
                     for (int k = 0; k < kUnit / 8; ++k)
                         *(u32x4*)(kt + off(write_at, i * kPer, k)) = widen(kr[i], k);
-            if (more) load(kr, keys, t0 + kStride, next_page);
+            if constexpr (kHalves) load(vr, values, t0, page);
+            else if (more) load(kr, keys, t0 + kStride, next_page);
         };
         auto store_values = [&] {
             if (lane_in)
@@ -411,7 +438,10 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
                         if (mixed) odd |= special4(v);
                         *(u32x4*)(vt + off(write_at, i * kPer, k)) = v;
                     }
-            if (more) load(vr, values, t0 + kStride, next_page);
+            if (more) {
+                if constexpr (kHalves) load(kr, keys, t0 + kStride, next_page);
+                else load(vr, values, t0 + kStride, next_page);
+            }
         };
         // A weight of zero does not hide an infinity or a NaN from rows that do not see its
         // token.  Such values are noted for the rows that do, and taken as zero.
@@ -452,10 +482,9 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
             if (part && t0 + part * kAttendTokens >= last) break;
             const int in_tile = part * kAttendTokens;
             // whether these tokens count for the wavefront's last tile
-            const bool last_too = !SHARED ? full == TILES : left ? wave < left * takers && (t0 - first + in_tile) / kAttendTokens % takers == wave % takers : full == TILES;
-            u32x4 p[TILES] = {}; // weights
-            // the weights of tiles from .. to - 1 of the wavefront
-            auto score = [&](auto from, auto to) {
+            const bool last_too = left ? wave < left * takers && (t0 - first + in_tile) / kAttendTokens % takers == wave % takers : full == TILES;
+            // scores, weights and sums of tiles from .. to - 1
+            auto pass = [&](auto from, auto to) {
                 f32x4 x[to - from][2] = {};
 #pragma unroll
                 for (int e = 0; e < kSteps; ++e) {
@@ -470,6 +499,22 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
                         for (int u = 0; u < 2; ++u) x[i - from][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u], y, x[i - from][u], 0, 0, 0);
                     }
                 }
+                if constexpr (!SHARED) {
+                    sync(); // the keys are read
+                    store_values();
+                    sync();
+                    if (mixed) take_out();
+                }
+                // values of four tokens of each half, a column to each lane: tokens u * 16 + g * 4 + j
+                auto value = [&](int e) {
+                    s16x4 half[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        half[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + off(value_at, in_tile + u * 16, 2 * e)));
+                    const u32x2 lo = __builtin_bit_cast(u32x2, half[0]), hi = __builtin_bit_cast(u32x2, half[1]);
+                    return __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+                };
+                bf16x8 p[to - from] = {};
 #pragma unroll
                 for (int i = from; i < to; ++i) {
                     if (i < TILES - 1 && i >= full) continue;
@@ -510,39 +555,27 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
                     sum[i] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
                     // rounded to bf16, as the matrix cores take them: half a step of 2^-8 each, as the
                     // outputs' own rounding is
-                    p[i] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
+                    p[i - from] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])});
                 }
-            };
-            auto weigh = [&](auto from, auto to) { // out^T += V^T P^T
+                // out^T += V^T P^T
 #pragma unroll
                 for (int e = 0; e < kOut; ++e) {
-                    s16x4 v[2]; // values of four tokens of each half, a column to each lane: tokens u * 16 + g * 4 + j
+                    const bf16x8 a = value(e);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + off(value_at, in_tile + u * 16, 2 * e)));
-                    const u32x2 lo = __builtin_bit_cast(u32x2, v[0]), hi = __builtin_bit_cast(u32x2, v[1]);
-                    const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
-#pragma unroll
-                    for (int i = from; i < to; ++i)
-                        acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, p[i]), acc[i][e], 0, 0, 0);
+                    for (int i = from; i < to; ++i) acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, p[i - from], acc[i][e], 0, 0, 0);
                 }
             };
             constexpr std::integral_constant<int, 0> kFirst;
             constexpr std::integral_constant<int, TILES - 1> kLast;
             constexpr std::integral_constant<int, TILES> kEnd;
             if constexpr (SHARED) {
-                if (TILES > 1 && full) {
-                    if constexpr (TILES > 1) score(kFirst, kLast), weigh(kFirst, kLast);
+                if constexpr (TILES > 1) {
+                    if (full) pass(kFirst, kLast);
                 }
                 // (left out where another wavefront takes it: weights of zero would make NaN of an infinity)
-                if (last_too) score(kLast, kEnd), weigh(kLast, kEnd);
+                if (last_too) pass(kLast, kEnd);
             } else {
-                score(kFirst, kEnd);
-                sync(); // the keys are read
-                store_values();
-                sync();
-                if (mixed) take_out();
-                weigh(kFirst, kEnd);
+                pass(kFirst, kEnd);
             }
         }
         sync(); // the tile is read
@@ -566,7 +599,7 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
         if (!whole) {
             *(f32x4*)(parts + m * DIM + d) = x;
         } else if (d < q.dim) {
-            const int row = (m + row0) / q.group, h = head * q.group + (m + row0) % q.group;
+            const int row = row_of(m + row0), h = head * q.group + m + row0 - row * q.group;
             const float by = all == 0.0f ? 0.0f : vscale / all;
             unsigned short* to = q.out + (q.r.roff ? (s.first + row) * q.orow : b * q.ob + row * q.orow) + h * q.oh + d;
             *(u32x2_any*)to = u32x2{pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by)};
@@ -577,7 +610,7 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
             parts[kRows * DIM + 2 * m] = most;
             parts[kRows * DIM + 2 * m + 1] = all;
         } else if (q.lse) {
-            const int row = (m + row0) / q.group, h = head * q.group + (m + row0) % q.group;
+            const int row = row_of(m + row0), h = head * q.group + m + row0 - row * q.group;
             const long long line = q.r.roff ? s.first + row : (long long)b * q.r.rows + row;
             q.lse[line * (q.kv_heads * q.group) + h] = all == 0.0f ? -INFINITY : (most + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f;
         }
@@ -615,11 +648,11 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     };
     // puts tile i of every wavefront there
     auto bring = [&](int i) {
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int e = 0; e < kOut; ++e) *(f32x4*)(meet + (wave * 16 + n16) * kMergeRow + e * 16 + g * 4) = acc[i][e];
         if (g == 0) refs[wave][n16] = top[i], sums[wave][n16] = sum[i];
-        __syncthreads();
+        lds_barrier();
     };
     if constexpr (SHARED) {
 #pragma unroll
@@ -646,19 +679,21 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
 }
 
 // Joins the pieces of a row and head: DIM / 4 lanes hold its columns, `parts` such
-// groups take every parts-th piece and meet in LDS.
+// groups take every parts-th piece and meet in LDS.  There is a column of workgroups for
+// each share but the first; it does the sequence whose second piece begins the share.
 template <int DIM>
-__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int b1, int rows, int parts)
+__global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int rows, int parts)
 {
     constexpr int kLanes = DIM / 4;
     __shared__ f32x4 meet[kThreads];
     __shared__ float refs[kThreads / kLanes], sums[kThreads / kLanes];
-    const int b = q.b0 + b1 + blockIdx.y;
-    const int base = b > q.b0 ? cache_uniform(q.ends + b - 1) : 0, end = cache_uniform(q.ends + b);
-    const int width = (cache_uniform(q.ends + q.b0 + q.B - 1) + q.shares - 1) / q.shares;
-    if (base == end) return;
+    const int share = blockIdx.y + 1, in = cache_uniform(q.starts + share);
+    if (in >= q.B) return;
+    const int b = q.b0 + in;
+    const int base = in ? cache_uniform(q.ends + in - 1) : 0, end = cache_uniform(q.ends + in);
+    const int width = (cache_uniform(q.ends + q.B - 1) + q.shares - 1) / q.shares;
     const int first = (base + kAttendBegin) / width, last = (end - 1) / width; // shares that have some of it
-    if (first == last) return;
+    if (share != first + 1 || share > last) return;
     const Sequence s = sequence_within(q, b);
     if (s.count <= 0) return;
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes, part = group % parts;
@@ -729,20 +764,18 @@ template <int DIM, bool E4M3, int TILES, bool SHARED>
 hipError_t launch_attend(const Attend& q, int batch, hipStream_t s)
 {
     const long long groups = (long long)(q.shares + 7) / 8 * 8 * q.kv_heads * q.blocks; // (at most 1024 * 1024 * 86 * 8 / 8)
-    int parts = 1; // groups that join a row: half as many as it may have pieces
-    while (parts * 2 <= kThreads / (DIM / 4) && parts * 2 < q.shares) parts *= 2;
+    // groups that join a row: half as many as a sequence has pieces if all have as many
+    int parts = 1;
+    while (parts * 2 <= kThreads / (DIM / 4) && parts * 2 < q.shares / std::min(q.B, batch)) parts *= 2;
     const int each = kThreads / (DIM / 4) / parts;
-    const unsigned join = (unsigned)(((long long)q.r.rows * q.kv_heads * q.group + each - 1) / each);
+    const dim3 join((unsigned)(((long long)q.r.rows * q.kv_heads * q.group + each - 1) / each), (unsigned)(q.shares - 1));
     hipError_t e = hipSuccess;
     Attend a = q;
     for (a.b0 = 0; a.b0 < q.B && e == hipSuccess; a.b0 += batch) {
         a.B = std::min(q.B - a.b0, batch);
         e = launch_kernel(sv_attend_kernel<DIM, E4M3, TILES, SHARED>, dim3((unsigned)groups), dim3(kThreads), 0, s, nullptr, nullptr, a);
         if (!q.ends || e != hipSuccess) continue;
-        const int most = (int)std::max(1ll, std::min<long long>(65535, 0xffffffffll / kThreads / join)); // of a launch
-        for (int b1 = 0; b1 < a.B && e == hipSuccess; b1 += most)
-            e = launch_kernel(sv_attend_join_kernel<DIM>, dim3(join, (unsigned)std::min(a.B - b1, most)), dim3(kThreads), 0, s, nullptr, nullptr,
-                              a, b1, TILES * 16 * (SHARED ? kAttendWaves : 1), parts);
+        e = launch_kernel(sv_attend_join_kernel<DIM>, join, dim3(kThreads), 0, s, nullptr, nullptr, a, TILES * 16 * (SHARED ? kAttendWaves : 1), parts);
     }
     return e;
 }
@@ -804,7 +837,7 @@ int64_t spec_verify_attend_workspace_bytes(const spec_verify_config* cfg, const 
     if (a->B == 0) return 0;
     const sv::AttendPlan p = plan_of(a);
     if (!may_split(a)) return 0;
-    return parts_bytes(a, p) + ((int64_t)a->B * 4 + 15) / 16 * 16;
+    return parts_bytes(a, p) + ((int64_t)(p.batch + p.shares) * 4 + 15) / 16 * 16;
 }
 
 int spec_verify_attend_check(const spec_verify_config* cfg, const spec_verify_attend_args* a)
@@ -868,6 +901,7 @@ int spec_verify_attend(spec_verify_t* h, const spec_verify_attend_args* a, void*
     q.shares = p.shares;
     q.parts = (float*)a->workspace;
     q.ends = may_split(a) ? (int*)((char*)a->workspace + parts_bytes(a, p)) : nullptr;
+    q.starts = q.ends + p.batch;
     q.status = a->device_status;
     e = e4m3 ? launch_dim<true>(q, p, s) : launch_dim<false>(q, p, s);
     return e == hipSuccess ? SV_OK : SV_EDEVICE;

@@ -9,7 +9,7 @@ constexpr int kAttendTokens = 32;  // tokens that a wavefront takes at a time
 constexpr int kAttendWaves = 4;
 constexpr int kAttendUnit = kAttendTokens * kAttendWaves; // tokens by which work is shared out
 constexpr int kAttendBegin = 2;    // units that beginning and ending a sequence counts for
-constexpr int kAttendBatch = 1024; // most sequences of a launch
+constexpr int kAttendBatch = 256;  // most sequences of a launch
 
 struct AttendPlan {
     bool shared;   // the wavefronts share the tokens and split the rows, not the other way round

@@ -190,7 +190,7 @@ int main()
                     for (int kv : {1, 5, 16, 1024}) {
                         const sv::AttendPlan p = sv::attend_plan(B, kv, dims[d], rows % 2, rows, len);
                         if ((long long)p.blocks * p.rows < rows || p.blocks < 1 || p.rows != p.tiles * (p.shared ? 64 : 16)) return printf("rows %lld\\n", rows), 1;
-                        if (p.batch < 1 || p.batch > B || p.batch > 1024 || p.shares < 8 || p.shares % 8) return printf("B %lld\\n", B), 1;
+                        if (p.batch < 1 || p.batch > B || p.batch > 256 || p.shares < 8 || p.shares % 8) return printf("B %lld\\n", B), 1;
                         // the units of a launch, and what is rounded up, stay within 32 bits, and so do its work-items
                         if (p.batch * (sv::attend_units(len) + sv::kAttendBegin) + p.shares > 0x7fffffffll) return printf("len %lld\\n", len), 1;
                         if ((long long)p.shares * kv * p.blocks * 256 > 0xffffffffll) return printf("groups %d %d %d\\n", p.shares, kv, p.blocks), 1;

@@ -21,6 +21,7 @@ using sv::kAttendTokens;
 using sv::kAttendUnit;
 using sv::kAttendWaves;
 using sv::launch_kernel;
+using sv::lds_barrier;
 using sv::Sequence;
 
 namespace {
@@ -77,14 +78,6 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-}
-
-// A barrier for LDS alone: what is under way from and to memory stays so.
-__device__ __forceinline__ void lds_barrier()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // The tokens that a sequence's rows see.

@@ -31,6 +31,14 @@ __device__ __forceinline__ void cache_status(int* status, int bits)
     if (status) __hip_atomic_fetch_or(status, bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// A barrier for LDS alone: what is under way from and to memory stays so.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // A value that every lane reads alike and no kernel of the call writes, through
 // the scalar cache.
 template <typename T>

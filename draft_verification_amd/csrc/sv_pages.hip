@@ -13,6 +13,7 @@ using sv::cache_uniform;
 using sv::Cache;
 using sv::DeviceGuard;
 using sv::launch_kernel;
+using sv::lds_barrier;
 using sv::Sequence;
 
 namespace {
@@ -70,9 +71,9 @@ __device__ __forceinline__ int block_before(int x, int* part, int& total)
         const int y = __shfl_up(sum, d);
         if (lane >= d) sum += y;
     }
-    __syncthreads(); // the last use of part
+    lds_barrier(); // the last use of part
     if (lane == 63) part[wave] = sum;
-    __syncthreads();
+    lds_barrier();
     int before = 0;
     total = 0;
 #pragma unroll
@@ -103,15 +104,20 @@ __device__ __forceinline__ unsigned free_word(const Cache& c, int w)
 }
 
 // RESERVE, and the new pages of FORK: one workgroup, since every page that is given
-// depends on all that are given before.  It counts what each sequence needs, sums
-// that up, and walks the bitmap of free pages, 32768 of them at a time, whose free
-// ones it lists in LDS, up to the last one needed.
+// depends on all that are given before.  It counts what each sequence needs, sums that
+// up, and walks the bitmap of free pages, 32768 of them at a time, whose free ones it
+// lists in LDS, up to the last one needed.  Bound by the steps that wait for one
+// another, and with many pages by what one compute unit stores: 16 sequences that need
+// 94 pages each GIVE16 us, 256 that need 750 GIVE256.
 __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
 {
-    constexpr int kEach = SV_MAX_PAGE_BATCH / kPlan; // sequences of a thread
+    constexpr int kEach = SV_MAX_PAGE_BATCH / kPlan; // most sequences of a thread
+    constexpr int kCount = 8;                        // words of a thread at a time where they are only counted
     __shared__ int key[kHash];             // slots that the call names, by hash
     __shared__ unsigned twice[kHash / 32]; // named again
     __shared__ int upto[SV_MAX_PAGE_BATCH]; // pages needed up to and with each sequence
+    __shared__ int slots[SV_MAX_PAGE_BATCH];
+    __shared__ int place[SV_MAX_PAGE_BATCH]; // RESERVE: pages that it has; FORK: the page to copy
     __shared__ unsigned short list[kPlan * 32];
     __shared__ int part[kPlan / 64];
     __shared__ int said;
@@ -119,14 +125,17 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const bool fork = q.kind == SV_PAGES_FORK;
     const int words = (c.n_pages + 31) / 32;
+    const int each = (q.B + kPlan - 1) / kPlan, b0 = tid * each; // sequences of a thread, one after the other
 
     for (int i = tid; i < kHash; i += kPlan) key[i] = -1;
     for (int i = tid; i < kHash / 32; i += kPlan) twice[i] = 0;
     if (tid == 0) said = 0;
-    __syncthreads();
-    auto slot_at = [&](int b) { return q.slots ? q.slots[b] : b; };
-    for (int b = tid; b < q.B; b += kPlan) {
-        const int slot = slot_at(b);
+    lds_barrier();
+    for (int i = 0; i < each; ++i) {
+        const int b = b0 + i;
+        if (b >= q.B) break;
+        const int slot = q.slots ? q.slots[b] : b;
+        slots[b] = slot;
         if (slot < 0 || slot >= c.n_slots) continue;
         for (unsigned h = hash_of(slot);; h = (h + 1) % kHash) {
             const int was = atomicCAS(&key[h], -1, slot);
@@ -134,24 +143,27 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
             if (was == -1 || was == slot) break;
         }
     }
-    __syncthreads();
+    lds_barrier();
     if (fork) { // a slot that is filled here is no source
-        for (int b = tid; b < q.B; b += kPlan) {
+        for (int i = 0; i < each; ++i) {
+            const int b = b0 + i;
+            if (b >= q.B) break;
             const int from = q.from[b];
-            const int h = from >= 0 && slot_at(b) != -1 ? hash_find(key, from) : -1;
+            const int h = from >= 0 && slots[b] != -1 ? hash_find(key, from) : -1;
             if (h >= 0) atomicOr(&twice[h / 32], 1u << (h % 32));
         }
-        __syncthreads();
+        lds_barrier();
     }
 
     // what each sequence needs: -1 nothing is to be done, -2 it is bad
     auto need_of = [&](int b) -> int {
-        const int slot = slot_at(b);
+        const int slot = slots[b];
         if (slot == -1) return -1;
         if (slot < 0 || slot >= c.n_slots) return -2;
         const int h = hash_find(key, slot);
-        if (twice[h / 32] >> (h % 32) & 1) return -2;
         const int held = held_pages(c, slot), len = c.lengths[slot];
+        place[b] = held;
+        if (twice[h / 32] >> (h % 32) & 1) return -2;
         if (held < 0 || len < 0) return -2;
         if (fork) {
             const int from = q.from[b];
@@ -160,6 +172,7 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
             if (n < 0 || pages < 0 || pages_for(c, n) > pages) return -2;
             if (!(n & ((1 << c.shift) - 1))) return 0;
             const int last = c.table[(long long)from * c.max_pages + (n >> c.shift)];
+            place[b] = last;
             return last < 0 || last >= c.n_pages ? -2 : 1;
         }
         const int n = counted_rows(q, b);
@@ -167,46 +180,47 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
         const long long pages = pages_for(c, (long long)len + n);
         return pages > c.max_pages ? -2 : pages > held ? (int)pages - held : 0;
     };
-    int need[kEach], mine = 0, total, bits = 0;
+    // sums stop at one page more than there are, which is too much already
+    const int most = c.n_pages + 1;
+    int need[kEach], mine = 0, total = 0, bits = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const int b = tid * kEach + i;
-        need[i] = b < q.B ? need_of(b) : -1;
+        need[i] = i < each && b0 + i < q.B ? need_of(b0 + i) : -1;
         if (need[i] == -2) bits |= SV_STATUS_BAD_INPUT;
-        // sums stop at one page more than there are, which is too much already
-        mine = min(mine + min(max(need[i], 0), c.n_pages + 1), c.n_pages + 1);
+        mine = min(mine + min(max(need[i], 0), most), most);
     }
     {
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const int y = __shfl_up(sum, d);
-            if (lane >= d) sum = min(sum + y, c.n_pages + 1);
+            if (lane >= d) sum = min(sum + y, most);
         }
         if (lane == 63) part[wave] = sum;
-        __syncthreads();
+        lds_barrier();
         int before = 0;
-        total = 0;
 #pragma unroll
         for (int w = 0; w < kPlan / 64; ++w) {
-            if (w < wave) before = min(before + part[w], c.n_pages + 1);
-            total = min(total + part[w], c.n_pages + 1);
+            if (w < wave) before = min(before + part[w], most);
+            total = min(total + part[w], most);
         }
         int run = __shfl_up(sum, 1);
-        run = min(before + (lane ? run : 0), c.n_pages + 1);
+        run = min(before + (lane ? run : 0), most);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int b = tid * kEach + i;
-            run = min(run + min(max(need[i], 0), c.n_pages + 1), c.n_pages + 1);
-            if (b < q.B) upto[b] = run;
+            if (i >= each || b0 + i >= q.B) break;
+            run = min(run + min(max(need[i], 0), most), most);
+            upto[b0 + i] = run;
         }
-        __syncthreads();
+        lds_barrier();
     }
     // how many pages are free, up to what is needed
     int have = 0;
-    for (int w0 = 0; w0 < words && have < total; w0 += kPlan) {
-        int found;
-        (void)block_before(__popc(w0 + tid < words ? free_word(c, w0 + tid) : 0u), part, found);
+    for (int w0 = 0; w0 < words && have < total; w0 += kPlan * kCount) {
+        int n = 0, found;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) n += __popc(w0 + i * kPlan + tid < words ? free_word(c, w0 + i * kPlan + tid) : 0u);
+        (void)block_before(n, part, found);
         have += found;
     }
     // all of the sequences whose sums stay below that; the sums do not fall
@@ -222,18 +236,20 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const int b = tid * kEach + i;
-        if (b >= q.B) continue;
+        const int b = b0 + i;
+        if (i >= each || b >= q.B) break;
         const bool ok = need[i] == 0 || (need[i] > 0 && upto[b] <= have);
         if (q.granted) q.granted[b] = ok;
         if (need[i] > 0 && !ok) bits |= SV_STATUS_NO_PAGES;
-        if (fork && need[i] <= 0) q.copies[b] = make_int2(-1, -1);
-        if (fork && need[i] > 0 && !ok) q.copies[b] = make_int2(-1, -1);
+        if (fork && !(need[i] > 0 && ok)) q.copies[b] = make_int2(-1, -1);
+        if (!fork && need[i] > 0 && ok) c.counts[slots[b]] = place[b] + need[i];
     }
     // the pages: the k-th free one to the sequence whose sums enclose k
     int base = 0;
+    unsigned ahead = tid < words ? free_word(c, tid) : 0u;
     for (int w0 = 0; w0 < words && base < given; w0 += kPlan) {
-        unsigned x = w0 + tid < words ? free_word(c, w0 + tid) : 0u;
+        unsigned x = ahead;
+        ahead = w0 + kPlan + tid < words ? free_word(c, w0 + kPlan + tid) : 0u;
         int found;
         int at = block_before(__popc(x), part, found);
         const int here = min(found, given - base);
@@ -243,7 +259,7 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
             taken |= x & -x;
         }
         if (taken) c.free[w0 + tid] &= ~taken;
-        __syncthreads();
+        lds_barrier();
         int lo = 0, hi = q.B; // first sequence that ends behind base
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
@@ -254,32 +270,20 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
             const int first = b ? upto[b - 1] : 0, end = min(upto[b], base + here);
             if (first >= base + here) break;
             if (first == upto[b]) continue;
-            const int slot = slot_at(b);
-            const long long row = (long long)slot * c.max_pages;
-            const int held = fork ? 0 : c.counts[slot];
+            int* const to = c.table + (long long)slots[b] * c.max_pages + place[b] - first;
             for (int k = max(first, base) + lane; k < end; k += 64) {
                 const int page = w0 * 32 + list[k - base];
                 c.refs[page] = 1;
-                if (fork) {
-                    const int from = q.from[b];
-                    q.copies[b] = make_int2(c.table[(long long)from * c.max_pages + (c.lengths[from] >> c.shift)], page);
-                } else {
-                    c.table[row + held + (k - first)] = page;
-                }
+                if (fork) q.copies[b] = make_int2(place[b], page);
+                else to[k] = page;
             }
         }
         base += found;
-        __syncthreads();
+        lds_barrier();
     }
-    if (!fork)
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int b = tid * kEach + i;
-            if (b < q.B && need[i] > 0 && upto[b] <= have) c.counts[slot_at(b)] += need[i];
-        }
     if (q.status) {
         if (bits) atomicOr(&said, bits);
-        __syncthreads();
+        lds_barrier();
         if (tid == 0) *q.status = said;
     }
 }
@@ -312,17 +316,20 @@ __global__ __launch_bounds__(kThreads) void sv_pages_share_kernel(Pages q)
     }
 }
 
-// COMMIT and RELEASE: a workgroup gives back one slot's pages past those it keeps.
+// COMMIT and RELEASE: a workgroup gives back one slot's pages past those it keeps, four
+// to a thread at a time.  Bound by the steps that wait for one another: the slot, its
+// numbers, its pages, their references.
 __global__ __launch_bounds__(kThreads) void sv_pages_back_kernel(Pages q)
 {
+    constexpr int kEach = 4;
     const int b = blockIdx.x;
     const Cache& c = q.c;
     const int slot = q.slots ? cache_uniform(q.slots + b) : b;
     if (slot == -1) return;
     bool bad = slot < 0 || slot >= c.n_slots;
+    const int held = bad ? -1 : held_pages(c, slot), len = bad ? -1 : c.lengths[slot];
     if (q.slots)
         for (int i = threadIdx.x; i < q.B; i += kThreads) bad |= i != b && q.slots[i] == slot;
-    const int held = bad ? -1 : held_pages(c, slot), len = bad ? -1 : c.lengths[slot];
     long long length = 0, keep = 0;
     if (q.kind == SV_PAGES_COMMIT) {
         const int n = counted_rows(q, b);
@@ -335,22 +342,35 @@ __global__ __launch_bounds__(kThreads) void sv_pages_back_kernel(Pages q)
         if (threadIdx.x == 0) cache_status(q.status, SV_STATUS_BAD_INPUT);
         return;
     }
-    const long long row = (long long)slot * c.max_pages;
-    for (int i = (int)keep + threadIdx.x; i < held; i += kThreads) {
-        const int page = c.table[row + i];
-        c.table[row + i] = -1;
-        const bool there = page >= 0 && page < c.n_pages;
-        const int refs = there ? atomicSub(&c.refs[page], 1) : 0;
-        if (refs == 1) {
-            atomicOr(&c.free[page / 32], 1u << (page % 32));
-        } else if (refs < 1) { // nothing that these calls leave
-            if (there) atomicAdd(&c.refs[page], 1);
-            cache_status(q.status, SV_STATUS_BAD_INPUT);
-        }
-    }
     if (threadIdx.x == 0) {
         c.lengths[slot] = (int)length;
         c.counts[slot] = (int)keep;
+    }
+    int* const row = c.table + (long long)slot * c.max_pages;
+    for (int i0 = (int)keep + threadIdx.x; i0 < held; i0 += kThreads * kEach) {
+        int page[kEach], refs[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = i0 + k * kThreads;
+            page[k] = i < held ? row[i] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const bool there = page[k] >= 0 && page[k] < c.n_pages;
+            refs[k] = there ? atomicSub(&c.refs[page[k]], 1) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = i0 + k * kThreads;
+            if (i >= held) break;
+            row[i] = -1;
+            if (refs[k] == 1) {
+                atomicOr(&c.free[page[k] / 32], 1u << (page[k] % 32));
+            } else if (refs[k] < 1) { // nothing that these calls leave
+                if (page[k] >= 0 && page[k] < c.n_pages) atomicAdd(&c.refs[page[k]], 1);
+                cache_status(q.status, SV_STATUS_BAD_INPUT);
+            }
+        }
     }
 }
 
@@ -372,55 +392,76 @@ __global__ __launch_bounds__(kThreads) void sv_pages_clear_kernel(Cache c)
 // tables are then changed.
 __global__ __launch_bounds__(kPlan) void sv_pages_pair_kernel(Pages q)
 {
+    constexpr int kEach = 4;
     __shared__ int part[kPlan / 64];
     const Cache& c = q.c;
     const int tid = threadIdx.x;
     const int words = (c.n_pages + 31) / 32;
-    int free = 0, total;
+    int free = 0, total, holes;
     for (int w = tid; w < words; w += kPlan) free += __popc(free_word(c, w));
     (void)block_before(free, part, total);
     const int live = c.n_pages - total;
-    // bits of a word at and above, or below, the number of pages in use
+    // bits of a word below the number of pages in use
     auto below = [&](int w) { const int n = live - w * 32; return n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u; };
-    int holes = 0;
-    for (int w0 = 0; w0 * 32 < live && holes < q.max_copies; w0 += kPlan) {
-        const int w = w0 + tid;
-        unsigned x = w < words ? free_word(c, w) & below(w) : 0u;
-        int found;
-        int at = holes + block_before(__popc(x), part, found);
-        for (; x && at < q.max_copies; x &= x - 1, ++at) q.copies[at].y = w * 32 + __ffs(x) - 1;
-        holes += found;
-    }
+    free = 0;
+    for (int w = tid; w < words; w += kPlan) free += __popc(free_word(c, w) & below(w));
+    (void)block_before(free, part, holes);
     const int moves = min(holes, q.max_copies);
-    int far = 0;
-    for (int w0 = words - 1; w0 >= 0 && far < moves; w0 -= kPlan) { // downwards
+    // upwards: the lowest free places are taken
+    for (int w0 = 0, done = 0; done < moves; w0 += kPlan) {
+        const int w = w0 + tid;
+        unsigned x = w < words ? free_word(c, w) & below(w) : 0u, used = 0;
+        int found;
+        int at = done + block_before(__popc(x), part, found);
+        for (; x && at < moves; x &= x - 1, ++at) {
+            q.copies[at].y = w * 32 + __ffs(x) - 1;
+            used |= x & -x;
+        }
+        if (used) c.free[w] &= ~used;
+        done += found;
+    }
+    // downwards: the highest pages leave theirs
+    for (int w0 = words - 1, done = 0; done < moves; w0 -= kPlan) {
         const int w = w0 - tid;
-        unsigned x = 0;
+        unsigned x = 0, used = 0;
         if (w >= 0) {
             const int pages = c.n_pages - w * 32;
             x = ~free_word(c, w) & ~below(w);
             if (pages < 32) x &= (1u << pages) - 1;
         }
         int found;
-        int at = far + block_before(__popc(x), part, found);
+        int at = done + block_before(__popc(x), part, found);
         for (; x && at < moves; ++at) {
             const int bit = 31 - __clz((int)x);
             q.copies[at].x = w * 32 + bit;
             x ^= 1u << bit;
+            used |= 1u << bit;
         }
-        far += found;
+        if (used) c.free[w] |= used;
+        done += found;
     }
     __syncthreads();
-    for (int i = tid; i < q.max_copies; i += kPlan) {
-        if (i >= moves) {
-            q.copies[i] = make_int2(-1, -1);
-            continue;
+    for (int i0 = tid; i0 < q.max_copies; i0 += kPlan * kEach) {
+        int2 pair[kEach];
+        int refs[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = i0 + k * kPlan;
+            pair[k] = i < moves ? q.copies[i] : make_int2(-1, -1);
         }
-        const int from = q.copies[i].x, to = q.copies[i].y;
-        c.refs[to] = c.refs[from];
-        c.refs[from] = ~to;
-        atomicOr(&c.free[from / 32], 1u << (from % 32));
-        atomicAnd(&c.free[to / 32], ~(1u << (to % 32)));
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) refs[k] = pair[k].x >= 0 ? c.refs[pair[k].x] : 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = i0 + k * kPlan;
+            if (i >= q.max_copies) break;
+            if (pair[k].x >= 0) {
+                c.refs[pair[k].y] = refs[k];
+                c.refs[pair[k].x] = ~pair[k].y;
+            } else {
+                q.copies[i] = pair[k];
+            }
+        }
     }
     if (tid == 0 && q.status) *q.status = 0;
 }

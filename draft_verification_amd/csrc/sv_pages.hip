@@ -107,8 +107,13 @@ __device__ __forceinline__ unsigned free_word(const Cache& c, int w)
 // depends on all that are given before.  It counts what each sequence needs, sums that
 // up, and walks the bitmap of free pages, 32768 of them at a time, whose free ones it
 // lists in LDS, up to the last one needed.  Bound by the steps that wait for one
-// another, and with many pages by what one compute unit stores: 16 sequences that need
-// 94 pages each GIVE16 us, 256 that need 750 GIVE256.
+// another, and with many pages by what one compute unit stores.  So many pages are given
+// in two launches: in the first a workgroup for every 32768 pages writes the tables and
+// the references, each having summed up for itself (GIVE_TABLES), and the second does the
+// rest (GIVE_STATE).
+enum { GIVE_ALL, GIVE_TABLES, GIVE_STATE };
+
+template <int PART>
 __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
 {
     constexpr int kEach = SV_MAX_PAGE_BATCH / kPlan; // most sequences of a thread
@@ -214,14 +219,23 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
         }
         lds_barrier();
     }
-    // how many pages are free, up to what is needed
-    int have = 0;
+    // how many pages are free, up to what is needed, and before the workgroup's own
+    const int own = PART == GIVE_TABLES ? (int)blockIdx.x * kPlan : 0;
+    int have = 0, base = 0;
     for (int w0 = 0; w0 < words && have < total; w0 += kPlan * kCount) {
-        int n = 0, found;
+        int n = 0, found, before = 0;
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) n += __popc(w0 + i * kPlan + tid < words ? free_word(c, w0 + i * kPlan + tid) : 0u);
+        for (int i = 0; i < kCount; ++i) {
+            const int w = w0 + i * kPlan + tid, k = __popc(w < words ? free_word(c, w) : 0u);
+            n += k;
+            if (PART == GIVE_TABLES && w < own) before += k;
+        }
         (void)block_before(n, part, found);
         have += found;
+        if constexpr (PART == GIVE_TABLES) {
+            (void)block_before(before, part, found);
+            base += found;
+        }
     }
     // all of the sequences whose sums stay below that; the sums do not fall
     int given = 0;
@@ -237,7 +251,7 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int b = b0 + i;
-        if (i >= each || b >= q.B) break;
+        if (PART == GIVE_TABLES || i >= each || b >= q.B) break;
         const bool ok = need[i] == 0 || (need[i] > 0 && upto[b] <= have);
         if (q.granted) q.granted[b] = ok;
         if (need[i] > 0 && !ok) bits |= SV_STATUS_NO_PAGES;
@@ -245,20 +259,24 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
         if (!fork && need[i] > 0 && ok) c.counts[slots[b]] = place[b] + need[i];
     }
     // the pages: the k-th free one to the sequence whose sums enclose k
-    int base = 0;
-    unsigned ahead = tid < words ? free_word(c, tid) : 0u;
-    for (int w0 = 0; w0 < words && base < given; w0 += kPlan) {
+    unsigned ahead = own + tid < words ? free_word(c, own + tid) : 0u;
+    for (int w0 = own; w0 < words && base < given && (PART != GIVE_TABLES || w0 == own); w0 += kPlan) {
         unsigned x = ahead;
         ahead = w0 + kPlan + tid < words ? free_word(c, w0 + kPlan + tid) : 0u;
         int found;
         int at = block_before(__popc(x), part, found);
         const int here = min(found, given - base);
         unsigned taken = 0;
+        if (PART == GIVE_STATE && at + __popc(x) <= here) taken = x, x = 0;
         for (; x && at < here; x &= x - 1, ++at) {
-            list[at] = (unsigned short)(tid * 32 + __ffs(x) - 1);
+            if constexpr (PART != GIVE_STATE) list[at] = (unsigned short)(tid * 32 + __ffs(x) - 1);
             taken |= x & -x;
         }
-        if (taken) c.free[w0 + tid] &= ~taken;
+        if (PART != GIVE_TABLES && taken) c.free[w0 + tid] &= ~taken;
+        if constexpr (PART == GIVE_STATE) {
+            base += found;
+            continue;
+        }
         lds_barrier();
         int lo = 0, hi = q.B; // first sequence that ends behind base
         while (lo < hi) {
@@ -281,7 +299,7 @@ __global__ __launch_bounds__(kPlan) void sv_pages_give_kernel(Pages q)
         base += found;
         lds_barrier();
     }
-    if (q.status) {
+    if (PART != GIVE_TABLES && q.status) {
         if (bits) atomicOr(&said, bits);
         lds_barrier();
         if (tid == 0) *q.status = said;
@@ -669,7 +687,15 @@ int spec_verify_pages(spec_verify_t* h, const spec_verify_pages_args* a, void* h
         e = clear_status(q.status, s);
         launch(sv_pages_back_kernel, q.B, kThreads, q);
     } else {
-        launch(sv_pages_give_kernel, 1, kPlan, q);
+        // us of a release and a reservation for 256 sequences of 512 in a pool of 600000 pages, in
+        // one launch and in two: 75 pages each 30 and 39, 150 each 36 and 41, 560 each 72 and 50
+        const long long may = q.kind == SV_PAGES_RESERVE ? (long long)q.B * ((q.rows >> q.c.shift) + 1) : 0;
+        if (may > 65536) {
+            launch(sv_pages_give_kernel<GIVE_TABLES>, (q.c.n_pages + 32 * kPlan - 1) / (32 * kPlan), kPlan, q);
+            launch(sv_pages_give_kernel<GIVE_STATE>, 1, kPlan, q);
+        } else {
+            launch(sv_pages_give_kernel<GIVE_ALL>, 1, kPlan, q);
+        }
         if (a->kind == SV_PAGES_FORK) launch(sv_pages_share_kernel, q.B, kThreads, q);
     }
     return status_of(e);

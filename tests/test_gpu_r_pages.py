@@ -251,6 +251,21 @@ def test_many_pages_and_sequences():
     s.reserve(slots[::3], rng.integers(1, 16000, 100))
 
 
+@pytest.mark.parametrize("n_pages", [70_000, 98_304, 150_001])
+def test_more_pages_than_one_workgroup_hands_out(n_pages):
+    # whole tiles of the bitmap and a part of one, requests that fit, that just fit and that do not
+    s = State(400, n_pages, 4, 400)
+    rng = np.random.default_rng(n_pages)
+    slots = list(rng.permutation(400)[:300])
+    s.reserve(slots[:50], rng.integers(1, 1600, 50))
+    s.release(slots[:50:2])  # holes
+    granted = s.reserve(slots, rng.integers(900, 1601, 300))
+    assert 0 in granted if n_pages < 90_000 else 1 in granted
+    s.commit(slots, [1] * 300)
+    s.release(slots[:250])
+    s.reserve(slots[:250] + slots[:3], [1600] * 253)  # three are named twice
+
+
 def test_the_largest_batch():
     s = State(4096, 9000, 4, 4)
     rng = np.random.default_rng(6)

@@ -16,7 +16,6 @@ using sv::cache_status;
 using sv::cache_uniform;
 using sv::DeviceGuard;
 using sv::kAttendBatch;
-using sv::kAttendBegin;
 using sv::kAttendTokens;
 using sv::kAttendUnit;
 using sv::kAttendWaves;
@@ -27,12 +26,6 @@ using sv::Sequence;
 namespace {
 
 constexpr int kThreads = 64 * kAttendWaves;
-
-// Wavefronts to a SIMD that the registers are shared out for.
-constexpr int attend_waves(int dim, bool e4m3, int tiles, bool shared)
-{
-    return shared ? 2 : dim == 64 ? (tiles == 1 ? 3 : 2) : e4m3 ? 2 : dim == 128 && tiles < 3 ? 2 : 1;
-}
 
 constexpr float kRoom = 16.0f; // how far (in log2) a score may lie above its row's reference
 
@@ -63,7 +56,7 @@ struct Attend {
     const float* vscale;
     float scale;
     int window, max_len;
-    int blocks, shares;
+    int blocks, shares, begin;
     int* ends;                  // [B]: where each sequence's units end among all of the launch; null: none is split
     int* starts;                // [shares]: the sequence in which each share begins
     float* parts;               // [shares][kv_heads][blocks][2]: sums of a workgroup, then its (reference, sum) pairs
@@ -104,16 +97,16 @@ __device__ __forceinline__ Sequence sequence_within(const Attend& q, int b)
 }
 
 // All sequences' units of tokens, one after the other, are cut into equal shares.  A
-// sequence counts kAttendBegin units more than it has, in front.  These are the units
+// sequence counts `begin` units more than it has, in front.  These are the units
 // from .. to - 1 of a sequence that ends at `end`, after one that ends at `base`, in a
 // share from lo to hi - 1 (from >= to: none).
 struct Piece {
     int from, to;
 };
 
-__device__ __forceinline__ Piece piece_of(int base, int end, int lo, int hi)
+__device__ __forceinline__ Piece piece_of(int begin, int base, int end, int lo, int hi)
 {
-    return Piece{max(0, max(lo, base) - base - kAttendBegin), max(0, min(hi, end) - base - kAttendBegin)};
+    return Piece{max(0, max(lo, base) - base - begin), max(0, min(hi, end) - base - begin)};
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -172,7 +165,7 @@ __device__ __forceinline__ const Attend* fresh_args()
 // SHARED = true, for many rows: each wavefront has rows of its own and they share a tile
 // of 64 tokens (32 of more than 128 columns) in LDS, so that no sums are held twice.
 template <int DIM, bool E4M3, int TILES, bool SHARED>
-__global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) void sv_attend_kernel(Attend args)
+__global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHARED)) void sv_attend_kernel(Attend args)
 {
     constexpr int kUnit = E4M3 ? 16 : 8;           // values of 16 bytes of the cache
     constexpr int kLanes = DIM / kUnit;            // lanes that read a token's row
@@ -223,7 +216,7 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
             if (s.count < 0 && blockIdx.x == 0) cache_status(args.status, SV_STATUS_BAD_INPUT);
             if (s.count > 0) {
                 const Reach reach = reach_of(args, s);
-                sum = (reach.end - reach.low + kAttendUnit - 1) / kAttendUnit + kAttendBegin;
+                sum = (reach.end - reach.low + kAttendUnit - 1) / kAttendUnit + args.begin;
             }
             known[threadIdx.x] = s;
         }
@@ -258,7 +251,7 @@ __global__ __launch_bounds__(kThreads, attend_waves(DIM, E4M3, TILES, SHARED)) v
     const int n16 = lane & 15, g = lane >> 4;
     const int base = next ? __builtin_amdgcn_readfirstlane(ends[next - 1]) : 0, end = __builtin_amdgcn_readfirstlane(ends[next]);
     if (base >= hi) break;
-    const Piece piece = piece_of(base, end, lo, hi);
+    const Piece piece = piece_of(q.begin, base, end, lo, hi);
     if (piece.from >= piece.to) continue;
     const int b = q.b0 + next;
     Sequence s;
@@ -685,7 +678,7 @@ __global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int 
     const int b = q.b0 + in;
     const int base = in ? cache_uniform(q.ends + in - 1) : 0, end = cache_uniform(q.ends + in);
     const int width = (cache_uniform(q.ends + q.B - 1) + q.shares - 1) / q.shares;
-    const int first = (base + kAttendBegin) / width, last = (end - 1) / width; // shares that have some of it
+    const int first = (base + q.begin) / width, last = (end - 1) / width; // shares that have some of it
     if (share != first + 1 || share > last) return;
     const Sequence s = sequence_within(q, b);
     if (s.count <= 0) return;
@@ -756,7 +749,7 @@ sv::AttendPlan plan_of(const spec_verify_attend_args* a)
 template <int DIM, bool E4M3, int TILES, bool SHARED>
 hipError_t launch_attend(const Attend& q, int batch, hipStream_t s)
 {
-    const long long groups = (long long)(q.shares + 7) / 8 * 8 * q.kv_heads * q.blocks; // (at most 1024 * 1024 * 86 * 8 / 8)
+    const long long groups = (long long)(q.shares + 7) / 8 * 8 * q.kv_heads * q.blocks;
     // groups that join a row: half as many as a sequence has pieces if all have as many
     int parts = 1;
     while (parts * 2 <= kThreads / (DIM / 4) && parts * 2 < q.shares / std::min(q.B, batch)) parts *= 2;
@@ -776,11 +769,17 @@ hipError_t launch_attend(const Attend& q, int batch, hipStream_t s)
 template <int DIM, bool E4M3>
 hipError_t launch_tiles(const Attend& q, const sv::AttendPlan& p, hipStream_t s)
 {
-    if constexpr (DIM < 256) {
-        if (p.tiles == 3) return p.shared ? launch_attend<DIM, E4M3, 3, true>(q, p.batch, s) : launch_attend<DIM, E4M3, 3, false>(q, p.batch, s);
-        if (p.tiles == 2) return p.shared ? launch_attend<DIM, E4M3, 2, true>(q, p.batch, s) : launch_attend<DIM, E4M3, 2, false>(q, p.batch, s);
+    constexpr int kSplit = DIM > 128 ? 1 : DIM / 64 + E4M3; // most tiles where tokens are split
+    if (!p.shared) {
+        if constexpr (kSplit >= 3) if (p.tiles == 3) return launch_attend<DIM, E4M3, 3, false>(q, p.batch, s);
+        if constexpr (kSplit >= 2) if (p.tiles == 2) return launch_attend<DIM, E4M3, 2, false>(q, p.batch, s);
+        return launch_attend<DIM, E4M3, 1, false>(q, p.batch, s);
     }
-    return p.shared ? launch_attend<DIM, E4M3, 1, true>(q, p.batch, s) : launch_attend<DIM, E4M3, 1, false>(q, p.batch, s);
+    if constexpr (DIM < 256) {
+        if (p.tiles == 3) return launch_attend<DIM, E4M3, 3, true>(q, p.batch, s);
+        if (p.tiles == 2) return launch_attend<DIM, E4M3, 2, true>(q, p.batch, s);
+    }
+    return launch_attend<DIM, E4M3, 1, true>(q, p.batch, s);
 }
 
 template <bool E4M3>
@@ -892,9 +891,10 @@ int spec_verify_attend(spec_verify_t* h, const spec_verify_attend_args* a, void*
     q.max_len = a->max_len ? a->max_len : a->cache.max_pages * a->cache.page_size;
     q.blocks = p.blocks;
     q.shares = p.shares;
+    q.begin = p.begin;
     q.parts = (float*)a->workspace;
     q.ends = may_split(a) ? (int*)((char*)a->workspace + parts_bytes(a, p)) : nullptr;
-    q.starts = q.ends + p.batch;
+    q.starts = q.ends ? q.ends + p.batch : nullptr;
     q.status = a->device_status;
     e = e4m3 ? launch_dim<true>(q, p, s) : launch_dim<false>(q, p, s);
     return e == hipSuccess ? SV_OK : SV_EDEVICE;

@@ -8,7 +8,6 @@ namespace sv {
 constexpr int kAttendTokens = 32;  // tokens that a wavefront takes at a time
 constexpr int kAttendWaves = 4;
 constexpr int kAttendUnit = kAttendTokens * kAttendWaves; // tokens by which work is shared out
-constexpr int kAttendBegin = 2;    // units that beginning and ending a sequence counts for
 constexpr int kAttendBatch = 256;  // most sequences of a launch
 
 struct AttendPlan {
@@ -17,10 +16,17 @@ struct AttendPlan {
     int rows;      // of a workgroup
     int blocks;    // workgroups for a block's rows
     int shares;    // equal shares of all sequences' tokens, of which each key-value head and block of rows takes all
+    int begin;     // units that beginning and ending a sequence counts for
     int batch;     // sequences of a launch
 };
 
 inline long long attend_units(long long tokens) { return (tokens + kAttendUnit - 1) / kAttendUnit; }
+
+// Workgroups of a compute unit, by the registers that the kernel needs.
+constexpr int attend_at_once(int dim, bool e4m3, int tiles, bool shared)
+{
+    return dim == 64 && tiles <= 1 + e4m3 ? 3 : dim > 128 && !shared && !e4m3 ? 1 : 2;
+}
 
 // dim: 64, 128 or 256 (the head's, rounded up).  rows: of all heads that share a
 // key-value head.  len: tokens that a sequence may see.
@@ -28,7 +34,11 @@ inline AttendPlan attend_plan(long long B, int kv_heads, int dim, bool e4m3, lon
 {
     AttendPlan p;
     const long long n = (rows + 15) / 16;
-    p.shared = n > (dim > 128 ? 1 : 3);
+    // us of 64 sequences of 200 to 8000 tokens and eight key-value heads, split by tokens and by
+    // rows: of 64 columns in bf16 one tile of rows 73 and 73, two 96 and 76; in e4m3 two 47 and
+    // 53, three 73 and 62; of 128 in bf16 two 129 and 134, three 179 and 141; in e4m3 three 95
+    // and 104 (four tiles' sums, or two of 256 columns, do not fit the registers of a wavefront)
+    p.shared = n > (dim > 128 ? 1 : dim / 64 + e4m3);
     if (p.shared) {
         const long long most = kAttendWaves * (dim > 128 ? 1 : 3); // tiles of a workgroup
         p.blocks = (int)((n + most - 1) / most);
@@ -38,10 +48,17 @@ inline AttendPlan attend_plan(long long B, int kv_heads, int dim, bool e4m3, lon
         p.tiles = (int)n;
     }
     p.rows = p.tiles * 16 * (p.shared ? kAttendWaves : 1);
-    // as many workgroups as the chip holds at once
-    const int at_once = dim == 64 ? 3 : !p.shared && !e4m3 && (dim == 256 || p.tiles == 3) ? 1 : 2;
+    // What a piece of a sequence takes beside its tokens is about that of 256 tokens, more where
+    // more tiles of rows meet at its end, less beside a large tile of tokens.  us with 1, 2 and 4
+    // units: of 64 columns in bf16, one tile of rows, 75, 77 and 81; of 128 in e4m3, three tiles,
+    // 104, 99 and 94, and one 74, 72 and 74; of 256 in bf16, one tile, 55, 60 and 67; of 128 in
+    // bf16, nine tiles, 534, 522 and 526
+    p.begin = !e4m3 && (dim > 128 || (!p.shared && p.tiles == 1)) ? 1 : !p.shared && p.tiles == 3 ? 4 : 2;
+    // As many workgroups as the chip holds at once.  Half as many, and twice: 72 and 64 us for 60,
+    // 92 and 72 for 76, 125 and 105 for 99, 817 and 549 for 519
+    const int at_once = attend_at_once(dim, e4m3, p.tiles, p.shared);
     const long long each = (long long)kv_heads * p.blocks;
-    const long long cost = attend_units(len) + kAttendBegin;
+    const long long cost = attend_units(len) + p.begin;
     p.batch = (int)((1ll << 30) / cost < kAttendBatch ? (1ll << 30) / cost : kAttendBatch);
     if (B < p.batch) p.batch = (int)B;
     long long shares = 256 * at_once / each / 8 * 8;

@@ -38,6 +38,15 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// A sequence that is cut, at the first share that does not begin it: its place in the launch
+// (none: -1), the shares that have some of it, its rows, and whether the first of these
+// shares has another sequence's piece in front.
+struct Cut {
+    int in, first, last, count;
+    int second, unused;
+    long long row;
+};
+
 struct Attend {
     sv::Cache c;
     sv::Rows r;
@@ -57,8 +66,7 @@ struct Attend {
     float scale;
     int window, max_len;
     int blocks, shares, begin;
-    int* ends;                  // [B]: where each sequence's units end among all of the launch; null: none is split
-    int* starts;                // [shares]: the sequence in which each share begins
+    struct Cut* cuts;           // [shares]: what the join of each has to know; null: no sequence is cut
     float* parts;               // [shares][kv_heads][blocks][2]: sums of a workgroup, then its (reference, sum) pairs
     int* status;
 };
@@ -157,13 +165,23 @@ __device__ __forceinline__ const Attend* fresh_args()
 // the right operand of out^T = V^T P^T, whose left operand LDS reads transposed.  A
 // row's maximum is not followed at every step: its reference stays as long as no
 // score lies more than 16 (in log2) above it, which keeps the weights below 2^16 and
-// spares the sums' rescaling (bf16 holds such weights as well as those below 1).
+// spares the sums' rescaling (bf16 holds such weights as well as those below 1).  That
+// is 519 us for the 596 of following it on 256 blocks of 17 rows.
 //
 // SHARED = false, for few rows: the four wavefronts take every fourth tile of 32 tokens,
 // each through its own part of LDS and with registers one tile ahead, without a barrier
 // until the end, where their sums are joined.
 // SHARED = true, for many rows: each wavefront has rows of its own and they share a tile
 // of 64 tokens (32 of more than 128 columns) in LDS, so that no sums are held twice.
+//
+// Bound by HBM where there are few rows: one request of 131000 tokens 4.9 TB/s in 109 us,
+// a token each of 64 requests, 282 MB, 4.0 TB/s in 71 (a large copy reaches 4.9, read and
+// write).  With more, by both HBM and what a tile costs in matrix, vector and LDS
+// instructions, which only partly overlap: 9 rows of 64 requests, 292 MB in e4m3, 93 us; 17
+// rows of 256 requests, 1.9 GB and 242 GFLOP, 527 us.
+//
+// Sequences are cut into equal shares rather than each into as many pieces: with lengths
+// that differ the longest one no longer decides (the 64 requests' tokens 82 us for 90).
 template <int DIM, bool E4M3, int TILES, bool SHARED>
 __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHARED)) void sv_attend_kernel(Attend args)
 {
@@ -179,7 +197,8 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
     constexpr int kTileBytes = kTile * DIM * 2;
     constexpr bool kTwo = SHARED;                  // keys and values in LDS of their own
     // Keys and values take turns in registers, each half a tile ahead, rather than both being one
-    // tile ahead.
+    // tile ahead: a drafting step of bf16 71 us for 79.  In e4m3, whose loads are half as many,
+    // the other way: a verify batch 99 us for 107.
     constexpr bool kHalves = !SHARED && !E4M3;
     // tiles whose queries stay in registers; the others' are in LDS
     constexpr int kQueryRegs = SHARED ? (DIM == 128 && TILES == 3 ? 1 : TILES) : TILES == 1 ? 1 : 0;
@@ -230,7 +249,6 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
         lds_barrier();
         for (int w = 0; w < wave; ++w) upto += place[w];
         ends[threadIdx.x] = upto;
-        if (args.ends && blockIdx.x == 0 && (int)threadIdx.x < args.B) args.ends[threadIdx.x] = upto;
         lds_barrier();
     }
     const int total = ends[args.B - 1], width = (total + args.shares - 1) / args.shares;
@@ -241,7 +259,14 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
         if (ends[next + half] <= lo) next += half + 1, n -= half + 1;
         else n = half;
     }
-    if (args.ends && head == 0 && block == 0 && threadIdx.x == 0) args.starts[share] = next;
+    if (args.cuts && head == 0 && block == 0 && threadIdx.x == 0) {
+        Cut cut = {-1};
+        if (next < args.B) {
+            const int base = next ? ends[next - 1] : 0, first = (base + args.begin) / width, last = (ends[next] - 1) / width;
+            if (share == first + 1 && share <= last) cut = {next, first, last, known[next].count, base > first * width, 0, known[next].first};
+        }
+        args.cuts[share] = cut;
+    }
     for (; next < args.B; ++next) {
     // What a piece needs is worked out anew for it: kept from piece to piece, it would take
     // the registers that the sums need.
@@ -666,43 +691,57 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
 
 // Joins the pieces of a row and head: DIM / 4 lanes hold its columns, `parts` such
 // groups take every parts-th piece and meet in LDS.  There is a column of workgroups for
-// each share but the first; it does the sequence whose second piece begins the share.
+// each share but the first; it does the sequence that is cut there first.
+// Bound by its chain of loads, and kept short by asking for kAhead pieces at once.
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int rows, int parts)
 {
-    constexpr int kLanes = DIM / 4;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    constexpr int kLanes = DIM / 4, kAhead = 4;
     __shared__ f32x4 meet[kThreads];
     __shared__ float refs[kThreads / kLanes], sums[kThreads / kLanes];
-    const int share = blockIdx.y + 1, in = cache_uniform(q.starts + share);
-    if (in >= q.B) return;
-    const int b = q.b0 + in;
-    const int base = in ? cache_uniform(q.ends + in - 1) : 0, end = cache_uniform(q.ends + in);
-    const int width = (cache_uniform(q.ends + q.B - 1) + q.shares - 1) / q.shares;
-    const int first = (base + q.begin) / width, last = (end - 1) / width; // shares that have some of it
-    if (share != first + 1 || share > last) return;
-    const Sequence s = sequence_within(q, b);
-    if (s.count <= 0) return;
+    const i32x4* const from_cut = (const i32x4*)(q.cuts + blockIdx.y + 1);
+    const i32x4 cut = cache_uniform(from_cut), more = cache_uniform(from_cut + 1);
+    if (cut[0] < 0) return;
+    const int b = q.b0 + cut[0], first = cut[1], last = cut[2], count = cut[3];
+    const long long row0 = (long long)((unsigned long long)(unsigned)more[3] << 32 | (unsigned)more[2]);
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes, part = group % parts;
-    const int heads = q.kv_heads * q.group, total = s.count * heads;
+    const int heads = q.kv_heads * q.group, total = count * heads;
     const int each = kThreads / kLanes / parts; // rows of a workgroup
     if ((int)blockIdx.x * each >= total) return;
     const int at = min((int)blockIdx.x * each + group / parts, total - 1); // row of the sequence, over all heads
-    const int head = at / (s.count * q.group), full = at % (s.count * q.group);
+    const int head = at / (count * q.group), full = at % (count * q.group);
     const int block = full / rows, m = full % rows;
     const long long size = (long long)rows * (DIM + 2), step = size * 2 * q.blocks * q.kv_heads;
     const float* from = q.parts + ((long long)head * q.blocks + block) * 2 * size;
-    // (only the share in which the sequence begins may have it in second place)
-    auto sums_of = [&](int share) { return from + share * step + (base > share * width ? size : 0); };
     float most = -FLT_MAX, all = 0.0f;
-#pragma unroll 4
-    for (int i = first + part; i <= last; i += parts) most = fmaxf(most, sums_of(i)[rows * DIM + 2 * m]);
     f32x4 x = {};
-#pragma unroll 4
-    for (int i = first + part; i <= last; i += parts) {
-        const float* of = sums_of(i);
-        const float factor = exp2_of(of[rows * DIM + 2 * m] - most);
-        all += factor * of[rows * DIM + 2 * m + 1];
-        x += factor * *(const f32x4*)(of + m * DIM + lane * 4);
+    for (int i = first + part; i <= last; i += parts * kAhead) {
+        float ref[kAhead], sum[kAhead];
+        f32x4 y[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int n = i + k * parts;
+            ref[k] = -FLT_MAX, sum[k] = 0.0f, y[k] = f32x4{};
+            if (n > last) continue;
+            const float* of = from + n * step + (n == first && more[0] ? size : 0);
+            ref[k] = of[rows * DIM + 2 * m];
+            sum[k] = of[rows * DIM + 2 * m + 1];
+            y[k] = *(const f32x4*)(of + m * DIM + lane * 4);
+        }
+        float top = most;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, ref[k]);
+        const float old = exp2_of(most - top);
+        all *= old;
+        x *= old;
+        most = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float factor = exp2_of(ref[k] - top);
+            all += factor * sum[k];
+            x += factor * y[k];
+        }
     }
     if (parts > 1) {
         meet[threadIdx.x] = x;
@@ -722,7 +761,7 @@ __global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int 
     if ((int)blockIdx.x * each + group / parts >= total) return;
     const int row = full / q.group, h = head * q.group + full % q.group, d = lane * 4;
     const float by = all == 0.0f ? 0.0f : (q.vscale ? q.vscale[head] : 1.0f) / all;
-    const long long line = q.r.roff ? s.first + row : (long long)b * q.r.rows + row;
+    const long long line = q.r.roff ? row0 + row : (long long)b * q.r.rows + row;
     unsigned short* to = q.out + (q.r.roff ? line * q.orow : b * q.ob + row * q.orow) + h * q.oh + d;
     if (d < q.dim) *(u32x2_any*)to = u32x2{pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by)};
     if (q.lse && lane == 0) q.lse[line * heads + h] = all == 0.0f ? -INFINITY : (most + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f;
@@ -760,7 +799,7 @@ hipError_t launch_attend(const Attend& q, int batch, hipStream_t s)
     for (a.b0 = 0; a.b0 < q.B && e == hipSuccess; a.b0 += batch) {
         a.B = std::min(q.B - a.b0, batch);
         e = launch_kernel(sv_attend_kernel<DIM, E4M3, TILES, SHARED>, dim3((unsigned)groups), dim3(kThreads), 0, s, nullptr, nullptr, a);
-        if (!q.ends || e != hipSuccess) continue;
+        if (!q.cuts || e != hipSuccess) continue;
         e = launch_kernel(sv_attend_join_kernel<DIM>, join, dim3(kThreads), 0, s, nullptr, nullptr, a, TILES * 16 * (SHARED ? kAttendWaves : 1), parts);
     }
     return e;
@@ -795,7 +834,7 @@ hipError_t launch_dim(const Attend& q, const sv::AttendPlan& p, hipStream_t s)
 // Whether a sequence may be too long for one unit.
 bool may_split(const spec_verify_attend_args* a) { return most_seen(a) > kAttendUnit; }
 
-// Workspace for the pieces of sequences that are split; behind it, where each ends.
+// Workspace for the pieces of sequences that are split; behind it, where they are cut.
 int64_t parts_bytes(const spec_verify_attend_args* a, const sv::AttendPlan& p)
 {
     return (int64_t)p.shares * a->kv.kv_heads * p.blocks * 2 * p.rows * (padded_dim(a->kv.head_dim) + 2) * 4;
@@ -829,7 +868,7 @@ int64_t spec_verify_attend_workspace_bytes(const spec_verify_config* cfg, const 
     if (a->B == 0) return 0;
     const sv::AttendPlan p = plan_of(a);
     if (!may_split(a)) return 0;
-    return parts_bytes(a, p) + ((int64_t)(p.batch + p.shares) * 4 + 15) / 16 * 16;
+    return parts_bytes(a, p) + (int64_t)p.shares * sizeof(Cut);
 }
 
 int spec_verify_attend_check(const spec_verify_config* cfg, const spec_verify_attend_args* a)
@@ -893,8 +932,7 @@ int spec_verify_attend(spec_verify_t* h, const spec_verify_attend_args* a, void*
     q.shares = p.shares;
     q.begin = p.begin;
     q.parts = (float*)a->workspace;
-    q.ends = may_split(a) ? (int*)((char*)a->workspace + parts_bytes(a, p)) : nullptr;
-    q.starts = q.ends ? q.ends + p.batch : nullptr;
+    q.cuts = may_split(a) ? (Cut*)((char*)a->workspace + parts_bytes(a, p)) : nullptr;
     q.status = a->device_status;
     e = e4m3 ? launch_dim<true>(q, p, s) : launch_dim<false>(q, p, s);
     return e == hipSuccess ? SV_OK : SV_EDEVICE;

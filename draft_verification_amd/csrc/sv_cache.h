@@ -39,7 +39,7 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// A value that every lane reads alike and no kernel of the call writes, through
+// A value that every lane reads alike and nothing writes while the kernel runs, through
 // the scalar cache.
 template <typename T>
 __device__ __forceinline__ T cache_uniform(const T* p)

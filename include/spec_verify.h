@@ -633,7 +633,7 @@ typedef struct {
     const int32_t* last_row;        /* RESERVE, COMMIT: optional device [B] */
     int32_t* granted;               /* FORK: device [B], 1 or 0 (0 also for -1 as a slot, and for bad ones);
                                        RESERVE: likewise, optional */
-    int32_t* copies;                /* FORK, COMPACT: device [max_copies][2] */
+    int32_t* copies;                /* FORK, COMPACT: device [max_copies][2], 8-byte aligned */
     int32_t max_copies;             /* FORK: >= B (entries past B are not written); COMPACT: 0 .. SV_MAX_PAGES */
     int32_t* device_status;         /* optional device [1] */
 } spec_verify_pages_args;
@@ -651,7 +651,7 @@ int spec_verify_pages(spec_verify_t* h, const spec_verify_pages_args* a, void* h
  */
 typedef struct {
     int32_t n_copies;               /* 0 .. SV_MAX_PAGES */
-    const int32_t* copies;          /* device [n_copies][2] */
+    const int32_t* copies;          /* device [n_copies][2], 8-byte aligned */
     void* pools;                    /* device */
     int32_t n_pools;                /* 1 .. 65535 */
     int64_t pool_stride;            /* bytes; >= n_pages * page_stride (one pool: not looked at) */
@@ -724,14 +724,16 @@ int spec_verify_append(spec_verify_t* h, const spec_verify_append_args* a, void*
  * values, the sum that divides them is taken before.  A row that sees nothing
  * (bad pages) is 0 and its lse -infinity.  What a row does not see, later rows of its
  * own block among it, does not change its result, infinities and NaN included.  Rows
- * that are not there keep their contents in both outputs.
+ * that are not there keep their contents in both outputs.  Sums are of weights up to
+ * 2^16: values up to 2^80 in magnitude cannot overflow in them.
  *
- * The length of a sequence is split over workgroups, whose parts are joined in a
- * fixed order: results are the same from run to run, but may differ in their last
- * bits with B, rows and max_len, which decide how it is split.
+ * The tokens of all sequences of a call are cut into equal shares, and the parts of a
+ * sequence that is cut are joined in a fixed order: results are the same from run to
+ * run, but may differ in their last bits with B, rows, max_len and the lengths of the
+ * other sequences, which decide where it is cut.
  *
  * workspace: spec_verify_attend_workspace_bytes(cfg, a) bytes, 16-byte aligned, the
- * caller's (it may be 0; a larger one will do).  Calls that overlap, and graphs that
+ * caller's (it may be 0; a larger one will do); what it holds before does not matter.  Calls that overlap, and graphs that
  * may be replayed at once, need one each.
  */
 typedef struct {

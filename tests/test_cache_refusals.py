@@ -68,6 +68,7 @@ def test_pages_refuses_caches(B, cfg, kind, more):
 @pytest.mark.parametrize("kind,field,value", [
     (1, "B", -1), (1, "B", 9), (1, "rows", -1), (1, "rows", (1 << 30) + 1), (2, "rows", -1), (3, "B", 9),
     (4, "granted", None), (4, "from_slots", None), (4, "copies", None), (4, "max_copies", 3), (5, "copies", None),
+    (4, "copies", FAKE + 4), (5, "copies", FAKE + 4),
     (5, "max_copies", -1), (5, "max_copies", (1 << 24) + 1), (1, "kind", 6), (1, "kind", -1),
 ])
 def test_pages_refuses(B, cfg, kind, field, value):
@@ -182,7 +183,7 @@ def test_attend_plan(tmp_path):
 int main()
 {
     const int dims[] = {64, 128, 256};
-    bool used[3][10] = {};
+    bool used[3][2][10] = {};
     for (int d = 0; d < 3; ++d)
         for (long long rows = 1; rows < 17000; rows += rows < 400 ? 1 : 37)
             for (long long len : {1ll, 127ll, 128ll, 129ll, 4000ll, 131000ll, 1ll << 30})
@@ -192,12 +193,12 @@ int main()
                         if ((long long)p.blocks * p.rows < rows || p.blocks < 1 || p.rows != p.tiles * (p.shared ? 64 : 16)) return printf("rows %lld\\n", rows), 1;
                         if (p.batch < 1 || p.batch > B || p.batch > 256 || p.shares < 8 || p.shares % 8) return printf("B %lld\\n", B), 1;
                         // the units of a launch, and what is rounded up, stay within 32 bits, and so do its work-items
-                        if (p.batch * (sv::attend_units(len) + sv::kAttendBegin) + p.shares > 0x7fffffffll) return printf("len %lld\\n", len), 1;
+                        if (p.batch * (sv::attend_units(len) + p.begin) + p.shares > 0x7fffffffll) return printf("len %lld\\n", len), 1;
                         if ((long long)p.shares * kv * p.blocks * 256 > 0xffffffffll) return printf("groups %d %d %d\\n", p.shares, kv, p.blocks), 1;
-                        used[d][p.tiles + 4 * p.shared] = true;
+                        used[d][rows % 2][p.tiles + 4 * p.shared] = true;
                     }
-    for (int d = 0; d < 3; ++d) {
-        for (int t = 1; t < 10; ++t) if (used[d][t]) printf(t > 4 ? "s%d " : "%d ", t > 4 ? t - 4 : t);
+    for (int d = 0; d < 6; ++d) {
+        for (int t = 1; t < 10; ++t) if (used[d / 2][d % 2][t]) printf(t > 4 ? "s%d " : "%d ", t > 4 ? t - 4 : t);
         printf("| ");
     }
 }
@@ -207,4 +208,4 @@ int main()
                     str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
-    assert r.stdout.strip() == "1 2 3 s1 s2 s3 | 1 2 3 s1 s2 s3 | 1 s1 |"
+    assert r.stdout.strip() == "1 s1 s2 s3 | 1 2 s1 s2 s3 | 1 2 s1 s2 s3 | 1 2 3 s1 s2 s3 | 1 s1 | 1 s1 |"

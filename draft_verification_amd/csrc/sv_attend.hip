@@ -174,11 +174,12 @@ __device__ __forceinline__ const Attend* fresh_args()
 // SHARED = true, for many rows: each wavefront has rows of its own and they share a tile
 // of 64 tokens (32 of more than 128 columns) in LDS, so that no sums are held twice.
 //
-// Bound by HBM where there are few rows: one request of 131000 tokens 4.9 TB/s in 109 us,
-// a token each of 64 requests, 282 MB, 4.0 TB/s in 71 (a large copy reaches 4.9, read and
-// write).  With more, by both HBM and what a tile costs in matrix, vector and LDS
-// instructions, which only partly overlap: 9 rows of 64 requests, 292 MB in e4m3, 93 us; 17
-// rows of 256 requests, 1.9 GB and 242 GFLOP, 527 us.
+// Bound by HBM where there are few rows, and by the 9 us that a launch's first sums take
+// (arguments, slots, lengths, pages, keys, values, one after the other): one request of
+// 131000 tokens 5.0 TB/s in 107 us, a token each of 64 requests, 282 MB, 4.0 TB/s in 70 (a
+// large copy reaches 4.9, read and write).  With more rows, by both HBM and what a tile
+// costs in matrix, vector and LDS instructions, which only partly overlap: 9 rows of 64
+// requests, 292 MB in e4m3, 90 us; 17 rows of 256 requests, 1.9 GB and 242 GFLOP, 516 us.
 //
 // Sequences are cut into equal shares rather than each into as many pieces: with lengths
 // that differ the longest one no longer decides (the 64 requests' tokens 82 us for 90).
@@ -692,7 +693,9 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
 // Joins the pieces of a row and head: DIM / 4 lanes hold its columns, `parts` such
 // groups take every parts-th piece and meet in LDS.  There is a column of workgroups for
 // each share but the first; it does the sequence that is cut there first.
-// Bound by its chain of loads, and kept short by asking for kAhead pieces at once.
+// Bound by its chain of loads (what is cut, sums), kept short by asking for kAhead pieces at
+// once: 4 us alone, 7 behind 64 requests of 9 rows, 18 (for 27 with a loop for the
+// references and one for the sums) behind 256 of 17.
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void sv_attend_join_kernel(Attend q, int rows, int parts)
 {

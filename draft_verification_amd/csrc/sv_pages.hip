@@ -107,7 +107,7 @@ __device__ __forceinline__ unsigned free_word(const Cache& c, int w)
 // depends on all that are given before.  It counts what each sequence needs, sums that
 // up, and walks the bitmap of free pages, 32768 of them at a time, whose free ones it
 // lists in LDS, up to the last one needed.  Bound by the steps that wait for one
-// another (slots, their numbers, the bitmap, the stores: 9 us for 16 sequences of 125
+// another (slots, their numbers, the bitmap, the stores: 8 us for 16 sequences of 125
 // pages), and with many pages by what one compute unit stores.  So many pages are given in
 // two launches: in the first a workgroup for every 32768 pages writes the tables and the
 // references, each having summed up for itself (GIVE_TABLES), and the second does the rest
@@ -524,7 +524,7 @@ struct Copy {
 constexpr int kCopyUnits = 4; // of 16 bytes for a thread
 
 // A piece of 16 KB of one page in one pool at a time.  Bound by HBM; neither side is
-// read again soon, so that both pass the caches by.
+// read again soon, so that both pass the caches by: 437 MB in 88 us (4.9 TB/s).
 __global__ __launch_bounds__(kThreads) void sv_pages_copy_kernel(Copy q)
 {
     for (long long job = blockIdx.x; job < q.total; job += gridDim.x) {
@@ -577,8 +577,8 @@ __device__ __forceinline__ unsigned to_e4m3(float a, float b, float c, float d)
 }
 
 // A thread takes 16 bytes of the cache: 8 values of bf16, or 16 of e4m3.  Bound by
-// HBM, 36 MB of 4352 rows in 8.3 us (4.3 TB/s with the launch) and 302 MB of prompts
-// to e4m3 in 72 (4.2 TB/s); e4m3 divides (fp32, correctly rounded) beside its loads.
+// HBM, 36 MB of 4352 rows in 7.9 us (4.5 TB/s with the launch) and 302 MB of prompts
+// to e4m3 in 62 to 67 (4.5 to 4.9 TB/s); e4m3 divides (fp32, correctly rounded) beside its loads.
 template <bool E4M3>
 __global__ __launch_bounds__(kThreads) void sv_append_kernel(Append q)
 {

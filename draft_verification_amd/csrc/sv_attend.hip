@@ -856,6 +856,7 @@ int check_sizes(const spec_verify_config* cfg, const spec_verify_attend_args* a)
     const spec_verify_cache& c = a->cache;
     if (c.max_pages < 1 || c.page_size < 1 || (long long)c.max_pages * c.page_size > SV_MAX_CACHE_TOKENS) return SV_EINVAL;
     if (a->B < 0 || a->B > cfg->max_batch || a->rows < 1 || a->row0 < 0 || (long long)a->row0 + a->rows > cfg->max_draft + 1) return SV_EINVAL;
+    if ((long long)a->rows * a->heads > 1 << 23) return SV_EUNSUPPORTED; // the join's work-items stay within 32 bits
     if (a->window < 0 || a->max_len < 0 || a->max_len > SV_MAX_CACHE_TOKENS) return SV_EINVAL;
     return SV_OK;
 }

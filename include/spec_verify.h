@@ -744,7 +744,7 @@ typedef struct {
     const int32_t* slots;           /* optional device [B] */
     const int32_t* last_row;        /* optional device [B] (dense rows only) */
     const int64_t* row_offsets;     /* optional device [B+1]: packed rows */
-    int32_t heads;                  /* a multiple of kv_heads, up to 64 times as many */
+    int32_t heads;                  /* a multiple of kv_heads, up to 64 times as many; rows * heads <= 2^23 */
     const void* queries;            /* device bf16; element (b, r, h, d) as append's rows are */
     int64_t query_batch_stride, query_row_stride, query_head_stride;
     void* outputs;                  /* device bf16, likewise; no overlap with the queries */

@@ -173,6 +173,15 @@ def test_attend_workspace(B, cfg):
         B.attend_workspace_bytes(cfg, a)
 
 
+def test_attend_refuses_more_rows_of_all_heads_than_a_launch_takes(B):
+    cfg = B.Config(8, 256, 100, B.SV_BF16, 0)
+    a = attend_args(B, kv=kv(B, kv_heads=1024, head_dim=64, strides=(1 << 20, 1 << 10, 64)), heads=65536, query_strides=(1 << 30, 1 << 22, 64),
+                    output_strides=(1 << 30, 1 << 22, 64), workspace_bytes=1 << 60)
+    for rows, rc in ((128, B.SV_OK), (129, B.SV_EUNSUPPORTED)):
+        a.rows = rows
+        assert B.attend_check(cfg, a) == rc
+
+
 def test_attend_plan(tmp_path):
     """Every row and every token has its workgroup, and the kernels that the plan names exist."""
     src = tmp_path / "plan.cpp"

@@ -440,6 +440,9 @@ __global__ __launch_bounds__(kPlan) void sv_pages_pair_kernel(Pages q)
         if (used) c.free[w] &= ~used;
         done += found;
     }
+    // the word that page `live` lies in is changed both ways, by two threads: what one has
+    // stored the other has to read (block_before's barriers are for LDS alone)
+    __syncthreads();
     // downwards: the highest pages leave theirs
     for (int w0 = words - 1, done = 0; done < moves; w0 -= kPlan) {
         const int w = w0 - tid;

@@ -548,12 +548,16 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
                     };
                     above();
                     if (__ballot(most > kRoom)) {
+                        // (a row's own scores alone move its reference: what other rows see of a token
+                        // that it does not see is not to change its last bits)
+                        float high = fmaxf(most, __shfl_xor(most, 16));
+                        high = fmaxf(high, __shfl_xor(high, 32));
                         most = -FLT_MAX;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) most = fmaxf(most, w[j] == -INFINITY ? -FLT_MAX : y[j / 4][j % 4] * scale);
                         most = fmaxf(most, __shfl_xor(most, 16));
                         most = fmaxf(most, __shfl_xor(most, 32));
-                        most = fmaxf(most, top[i]);
+                        most = high > kRoom ? fmaxf(most, top[i]) : top[i];
                         // (every lane takes part: sums that only some lanes change would be held twice)
                         const float factor = exp2_of(top[i] - most);
                         top[i] = most;

@@ -723,8 +723,9 @@ int spec_verify_append(spec_verify_t* h, const spec_verify_append_args* a, void*
  * is; the weights exp(s_t - max) are rounded to bf16 for their product with the
  * values, the sum that divides them is taken before.  A row that sees nothing
  * (bad pages) is 0 and its lse -infinity.  What a row does not see, later rows of its
- * own block among it, does not change its result, infinities and NaN included.  Rows
- * that are not there keep their contents in both outputs.  Sums are of weights up to
+ * own block among it, does not change a bit of its result, infinities and NaN included,
+ * and neither do the other rows' queries.  Rows that are not there keep their contents in
+ * both outputs.  Sums are of weights up to
  * 2^16: values up to 2^80 in magnitude cannot overflow in them.
  *
  * The tokens of all sequences of a call are cut into equal shares, and the parts of a

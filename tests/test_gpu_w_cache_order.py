@@ -8,6 +8,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from tests.test_gpu_r_pages import State  # noqa: E402
+from tests.test_gpu_t_attend import Call, _plant  # noqa: E402
 
 
 @pytest.mark.parametrize("n_pages", [64, 2000, 33_000, 70_001])
@@ -29,3 +30,33 @@ def test_compaction_changes_one_word_of_the_bitmap_both_ways(n_pages):
         moves = s.compact(8)
         assert [m for m in moves if m[0] >= 0] == [[live + holes - 1 - i, word + bit + i] for i in range(holes)]
         s.release([0, 2])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D,group", [(64, 2), (64, 12), (128, 2), (128, 20), (256, 1), (256, 16)])
+@pytest.mark.parametrize("length,kv", [(150, 2), (3000, 2), (1400, 64), (1500, 64)])
+def test_what_a_row_does_not_see_does_not_move_it(length, kv, D, group, e4m3):
+    """Finite keys and values of later rows of the block, and those rows' queries, to the last
+    bit: a large score of one row leaves the others' references where they are.  (With many
+    key-value heads a piece of a sequence is several tiles for each wavefront.)"""
+    rows, row = 6, 3
+    c = Call(300, [length, 20], rows, D=D, group=group, e4m3=e4m3, kv=kv)
+    p = c.paged
+    want, want_lse = c.run().result()
+    held = [x.clone() for x in p.pools]
+    by = c.q[row:rows, :group].double().numpy().sum(-1) * c.scale * (p.kscale[0] if e4m3 else 1.0)  # the token's score for a key of ones
+    key = 448.0 if e4m3 else 40.0
+    for which, value in ((0, key), (0, -key), (1, 400.0)):
+        out, lse = _plant(c, which, [length + row], value).run().result()
+        assert c.status.item() == 0
+        assert np.array_equal(out[:row], want[:row]) and np.array_equal(lse[:row], want_lse[:row])
+        assert np.array_equal(out[:, group:], want[:, group:]) and np.array_equal(out[rows:], want[rows:])
+        if which == 0:  # a score of 16 / log2(e) above a reference moves it
+            high = value * by > want_lse[row:rows, :group] + 12.0
+            assert (lse[row:rows, :group][high] > want_lse[row:rows, :group][high] + 11.0).all()
+        for x, dev, was in zip(p.pools, p.dev, held):
+            x.copy_(was), dev.copy_(was)
+    c.q_dev.view(-1, c.row)[row:rows] *= 30.0
+    out, lse = c.run().result()
+    assert np.array_equal(out[:row], want[:row]) and np.array_equal(lse[:row], want_lse[:row])
+    assert not np.array_equal(out[row:rows], want[row:rows]) and np.array_equal(out[rows:], want[rows:])

@@ -1,0 +1,32 @@
+"""Sizes that the calls on the paged cache take and refuse at the ends of their ranges, on the host
+(no GPU: the checks touch no device state)."""
+import os
+
+import pytest
+
+FAKE = 1 << 40  # an address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def B():
+    from draft_verification_amd import binding, build
+    if not os.path.exists(binding.LIB_PATH):
+        build.build()
+    return binding
+
+
+@pytest.fixture(scope="module")
+def cfg(B):
+    return B.Config(8, 8, 1000, B.SV_BF16, 0)
+
+
+def copies(B, **more):
+    d = dict(copies=FAKE, pools=FAKE, n_pools=3, pool_stride=100 * 512, page_stride=512, page_bytes=512, n_pages=100)
+    d.update(more)
+    return B.make_pages_copy_args(5, **d)
+
+
+@pytest.mark.parametrize("pool_stride", [0, -1, 8, (1 << 46) + 16, 1 << 62, -(1 << 63)])
+def test_the_stride_of_one_pool_is_not_looked_at(B, cfg, pool_stride):
+    assert B.pages_copy_check(cfg, copies(B, n_pools=1, pool_stride=pool_stride)) == B.SV_OK
+    assert B.pages_copy_check(cfg, copies(B, n_pools=2, pool_stride=pool_stride)) != B.SV_OK

@@ -720,7 +720,8 @@ int spec_verify_pages_copy_check(const spec_verify_config* cfg, const spec_verif
     if (a->n_pools < 1 || a->n_pools > 65535) return SV_EINVAL;
     if (a->page_bytes < 16 || a->page_bytes % 16 || a->page_stride < a->page_bytes || a->page_stride % 16) return SV_EINVAL;
     if (a->page_bytes > (1 << 30) || a->page_stride > (1ll << 40)) return SV_EUNSUPPORTED;
-    if (a->n_pools > 1 && (a->pool_stride % 16 || a->pool_stride < a->n_pages * a->page_stride)) return SV_EINVAL;
+    // (n_pages * page_stride might not fit 63 bits)
+    if (a->n_pools > 1 && (a->pool_stride % 16 || a->pool_stride / a->n_pages < a->page_stride)) return SV_EINVAL;
     if (a->n_pools > 1 && a->pool_stride > (1ll << 46)) return SV_EUNSUPPORTED;
     if (a->n_copies && (!a->copies || !a->pools || (uintptr_t)a->pools % 16 || (uintptr_t)a->copies % 8)) return SV_EINVAL;
     return SV_OK;

@@ -30,3 +30,14 @@ def copies(B, **more):
 def test_the_stride_of_one_pool_is_not_looked_at(B, cfg, pool_stride):
     assert B.pages_copy_check(cfg, copies(B, n_pools=1, pool_stride=pool_stride)) == B.SV_OK
     assert B.pages_copy_check(cfg, copies(B, n_pools=2, pool_stride=pool_stride)) != B.SV_OK
+
+
+@pytest.mark.parametrize("n_pages,page_stride", [(1 << 24, 1 << 40), ((1 << 24) - 1, 1 << 40), (1 << 23, 1 << 40),
+                                                 (12345678, 1 << 40), (1 << 24, (1 << 39) + 16), (1 << 24, (1 << 22) + 16)])
+def test_pools_that_overlap_are_refused_whatever_their_pages_take(B, cfg, n_pages, page_stride):
+    """n_pages * page_stride may lie past 63 bits."""
+    for pool_stride in (0, 512, page_stride, 1 << 46):
+        args = copies(B, n_pages=n_pages, page_stride=page_stride, pool_stride=pool_stride)
+        assert B.pages_copy_check(cfg, args) == B.SV_EINVAL
+    args = copies(B, n_pages=1 << 24, page_stride=1 << 22, pool_stride=1 << 46)  # that just fit
+    assert B.pages_copy_check(cfg, args) == B.SV_OK

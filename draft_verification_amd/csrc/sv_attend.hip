@@ -426,7 +426,8 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
         const int far_page = pages_of(t0 + 2 * kStride);
         __builtin_amdgcn_sched_barrier(0);
         const unsigned long long gone = __ballot(is_bad(page)); // tokens whose page is bad
-        if (gone && lane == 0) cache_status(q.status, SV_STATUS_BAD_INPUT);
+        // (those in front of every row's window, in the first tile, may be)
+        if (gone && is_bad(page) && (!q.window || t0 + (lane & (kTile - 1)) > s.start - q.window)) cache_status(q.status, SV_STATUS_BAD_INPUT);
         // some row does not see some token
         const bool mixed = t0 + kTile - 1 > s.start || gone || (q.window && t0 <= s.start + s.count - 1 - q.window);
         bool odd = false; // whether a value of a mixed tile is infinite or NaN

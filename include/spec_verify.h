@@ -562,7 +562,7 @@ int spec_verify_head(spec_verify_t* h, const spec_verify_head_args* a, void* hip
  * negative, descending or further apart than `rows`, a negative length, or rows
  * behind the pages that the slot holds (nothing is done for the sequence); a
  * page outside [0, n_pages) in a table (what would lie there is not written, and
- * not seen).  No call reads or writes outside the given buffers for any of them.
+ * not seen; pages in front of every row's window may be gone).  No call reads or writes outside the given buffers for any of them.
  */
 #define SV_MAX_PAGES (1 << 24)
 #define SV_MAX_PAGE_SIZE 1024

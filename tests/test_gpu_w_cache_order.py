@@ -60,3 +60,27 @@ def test_what_a_row_does_not_see_does_not_move_it(length, kv, D, group, e4m3):
     out, lse = c.run().result()
     assert np.array_equal(out[:row], want[:row]) and np.array_equal(lse[:row], want_lse[:row])
     assert not np.array_equal(out[row:rows], want[row:rows]) and np.array_equal(out[rows:], want[rows:])
+
+
+@pytest.mark.parametrize("D,group", [(64, 2), (128, 2), (128, 20), (256, 1), (256, 16)])
+@pytest.mark.parametrize("page", [1, 4, 16, 32])
+def test_pages_in_front_of_a_window_may_be_gone(page, D, group):
+    """A layer with a window needs no page in front of it: that none is named there is no error,
+    wherever the window begins within a tile."""
+    rows, window = 3, 100
+    for length in (110, 131, 147, 1000):
+        kind = dict(D=D, group=group, page=page, window=window)
+        want, want_lse = Call(310, [length, 40], rows, **kind).run().result()
+        c = Call(310, [length, 40], rows, **kind)
+        p = c.paged
+        first = length + 1 - window  # what row 0 sees first
+        p.table[p.slots[0], :first // page] = np.resize([-1, p.n_pages, 1 << 30], first // page)
+        p.d["table"].copy_(torch.from_numpy(p.table))
+        out, lse = c.run().result()
+        assert np.array_equal(out, want) and np.array_equal(lse, want_lse)
+        assert c.status.item() == 0
+        # one page further is seen
+        p.table[p.slots[0], first // page] = -1
+        p.d["table"].copy_(torch.from_numpy(p.table))
+        c.run().result()
+        assert c.status.item() == 1

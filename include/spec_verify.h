@@ -720,22 +720,27 @@ int spec_verify_append(spec_verify_t* h, const spec_verify_append_args* a, void*
  *   s_t = scale * <q, k_t>,  out = sum_t exp(s_t - lse) v_t,  lse = ln sum_t exp(s_t)
  * Queries and outputs are bf16, lse fp32.  Products are exact in fp32 (keys of
  * SV_KV_E4M3 meet their scale after the sum) and summed in fp32, as the softmax
- * is; the weights exp(s_t - max) are rounded to bf16 for their product with the
- * values, the sum that divides them is taken before.  A row that sees nothing
- * (bad pages) is 0 and its lse -infinity.  What a row does not see, later rows of its
- * own block among it, does not change a bit of its result, infinities and NaN included,
- * and neither do the other rows' queries.  Rows that are not there keep their contents in
- * both outputs.  Sums are of weights up to
- * 2^16: values up to 2^80 in magnitude cannot overflow in them.
+ * is; the weights, exp(s_t - ref) with ref less than 16 ln 2 below the largest score, are
+ * rounded to bf16 for their product with the values, the sum that divides them is taken
+ * before.  Sums are of weights up to 2^16: values up to 2^80 in magnitude cannot overflow
+ * in them.  A row that sees nothing (bad pages) is 0 and its lse -infinity.  What a row
+ * does not see, later rows of its own block among it, does not change a bit of its
+ * result, infinities and NaN included, and neither do the other rows' queries.  Rows that
+ * are not there keep their contents in both outputs.
+ * Of what a row sees: a score of -infinity weighs nothing (all of them: as if the row
+ * saw nothing); one of +infinity or NaN makes the row and its lse NaN.  An infinite value
+ * makes its element of the result infinite, or NaN if the token's weight is 0 or
+ * underflows on the way, which depends on where the sequence is cut (below); a NaN makes
+ * it NaN.  Other elements are as without.
  *
  * The tokens of all sequences of a call are cut into equal shares, and the parts of a
  * sequence that is cut are joined in a fixed order: results are the same from run to
- * run, but may differ in their last bits with B, rows, max_len and the lengths of the
- * other sequences, which decide where it is cut.
+ * run, but may differ in their last bits with B, rows, max_len, the sequence's own number
+ * of rows and the lengths of the other sequences, which decide where it is cut.
  *
  * workspace: spec_verify_attend_workspace_bytes(cfg, a) bytes, 16-byte aligned, the
- * caller's (it may be 0; a larger one will do); what it holds before does not matter.  Calls that overlap, and graphs that
- * may be replayed at once, need one each.
+ * caller's (it may be 0; a larger one will do); what it holds before does not matter.
+ * Calls that overlap, and graphs that may be replayed at once, need one each.
  */
 typedef struct {
     int32_t B, rows;                /* 0 <= B <= max_batch; 1 <= rows; row0 + rows <= max_draft + 1 */

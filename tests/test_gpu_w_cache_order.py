@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from tests.test_gpu_r_pages import State  # noqa: E402
-from tests.test_gpu_t_attend import Call, _plant  # noqa: E402
+from tests.test_gpu_t_attend import Call, _plant, bounds  # noqa: E402
 
 
 @pytest.mark.parametrize("n_pages", [64, 2000, 33_000, 70_001])
@@ -84,3 +84,88 @@ def test_pages_in_front_of_a_window_may_be_gone(page, D, group):
         p.d["table"].copy_(torch.from_numpy(p.table))
         c.run().result()
         assert c.status.item() == 1
+
+
+def _elements(c, which, token, d, what):
+    """Puts `what` into channel d of key-value head 0 of one token of sequence 0."""
+    p = c.paged
+    page = int(p.table[p.slots[0]][token // p.page])
+    p.view(p.pools[which])[page, 0, token % p.page, d] = what
+    p.dev[which].copy_(p.pools[which])
+
+
+@pytest.mark.parametrize("what", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("D,group", [(64, 2), (128, 2), (128, 20), (256, 1), (256, 16)])
+@pytest.mark.parametrize("length", [90, 700, 3000])
+def test_infinite_values_that_are_seen(length, D, group, what):
+    """They stay in their element, and none of it is lost: wherever the sequence is cut, in weights
+    that are large, small, and far below what fp32 holds."""
+    rows, at = 3, 7
+    for steep in (0.0, 4.0):  # with 4, scores rise by hundreds: most weights underflow
+        c = Call(320, [length, 30], rows, D=D, group=group)
+        p = c.paged
+        rise = torch.zeros((length + rows, 2, D))
+        rise[:, :, 0] = steep * torch.arange(length + rows)[:, None]
+        rise[:, :, 1:] = torch.from_numpy(p.exact[0][0]).float()[:, :, 1:]
+        p.fill(0, 0, rise.numpy())
+        p.dev[0].copy_(p.pools[0])
+        c.q[:, :, 0] = 4.0
+        c.q_dev.copy_(c.q.reshape(-1).to(c.q_dev))
+        want, want_lse = c.run().check()
+        held = p.pools[1].clone()
+        for token in (0, 40, length // 2, length - 1):
+            _elements(c, 1, token, at, what)
+            out, lse = c.run().result()
+            got = out[:rows, :group, at].copy()
+            out[:rows, :group, at] = want[:rows, :group, at]
+            assert np.array_equal(out, want) and np.array_equal(lse, want_lse)
+            if what != what:
+                assert np.isnan(got).all()
+            else:
+                assert (np.isnan(got) | (got == what)).all()
+                if not steep:
+                    assert (got == what).all()
+            p.pools[1].copy_(held)
+
+
+@pytest.mark.parametrize("D,group", [(64, 2), (128, 20), (256, 1), (256, 16)])
+@pytest.mark.parametrize("length", [90, 3000])
+def test_infinite_scores(length, D, group):
+    rows = 3
+    kind = dict(D=D, group=group)
+
+    def call():
+        c = Call(330, [length, 30], rows, **kind)
+        c.q[:, :, 0] = 1.0
+        c.q_dev.copy_(c.q.reshape(-1).to(c.q_dev))
+        return c
+    want, want_lse = call().run().check()
+    # -infinity: the token is as if it were not there
+    c = call()
+    gone = np.zeros(length + rows, bool)
+    for token in (0, 33, 64, length - 1):
+        _elements(c, 0, token, 0, -float("inf"))
+        gone[token] = True
+    out, lse = c.run().result()
+    assert c.status.item() == 0
+    o, l, size, extra = c.want(0, gone)
+    tol, ltol = bounds(D, length + rows, o, l, size, extra)
+    at = np.arange(group)  # heads of key-value head 0
+    assert (np.abs(out[:rows] - o) <= tol)[:, at].all() and (np.abs(lse[:rows] - l) <= ltol)[:, at].all()
+    assert np.array_equal(out[:, group:], want[:, group:]) and np.array_equal(lse[:, group:], want_lse[:, group:])
+    # all of them: as if the row saw nothing
+    c = call()
+    raw = c.paged.view(c.paged.pools[0])
+    raw[torch.from_numpy(c.paged.table[c.paged.slots[0]].astype(np.int64)).clamp(min=0).unique(), 0, :, 0] = -float("inf")
+    c.paged.dev[0].copy_(c.paged.pools[0])
+    out, lse = c.run().result()
+    assert (out[:rows, :group] == 0).all() and (lse[:rows, :group] == -np.inf).all()
+    assert np.array_equal(out[:, group:], want[:, group:])
+    # +infinity, seen by the last row alone and by all
+    for token, first in ((length + rows - 1, rows - 1), (5, 0)):
+        c = call()
+        _elements(c, 0, token, 0, float("inf"))
+        out, lse = c.run().result()
+        assert np.isnan(out[first:rows, :group]).all() and np.isnan(lse[first:rows, :group]).all()
+        out[first:rows, :group], lse[first:rows, :group] = want[first:rows, :group], want_lse[first:rows, :group]
+        assert np.array_equal(out, want) and np.array_equal(lse, want_lse)

@@ -169,3 +169,35 @@ def test_infinite_scores(length, D, group):
         assert np.isnan(out[first:rows, :group]).all() and np.isnan(lse[first:rows, :group]).all()
         out[first:rows, :group], lse[first:rows, :group] = want[first:rows, :group], want_lse[first:rows, :group]
         assert np.array_equal(out, want) and np.array_equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("D,group", [(64, 16), (64, 64), (128, 64), (256, 8), (256, 64)])
+def test_every_e4m3_code(D, group):
+    """A row that sees one token gets that token's values, exactly; with queries of one channel
+    each, lse is that channel of the key, within lse's rounding."""
+    kv = 256 // group
+    c = Call(340, [0], 1, D=D, group=group, kv=kv, e4m3=True, scaled=False, page=1, scale=1.0)
+    p = c.paged
+    codes = torch.arange(256, dtype=torch.uint8)
+    page = int(p.table[p.slots[0]][0])
+    # values: all codes, D to a key-value head, over and over
+    of_value = codes.repeat(kv * D // 256 + 1)[:kv * D].view(kv, D)
+    p.view(p.pools[1].view(torch.uint8))[page, :, 0] = of_value
+    # keys: of each key-value head the channels that its queries ask for, all codes in all
+    ask = min(group, D)
+    of_key = torch.zeros((kv, D), dtype=torch.uint8)
+    of_key[:, :ask] = codes.repeat(kv * ask // 256 + 1)[:kv * ask].view(kv, ask)
+    of_key[(of_key & 0x7f) == 0x7f] = 0  # (not a number: felt by every query)
+    p.view(p.pools[0].view(torch.uint8))[page, :, 0] = of_key
+    for dev, pool in zip(p.dev, p.pools):
+        dev.copy_(pool)
+    c.q.zero_()
+    c.q.view(kv, group, D)[:, torch.arange(group), torch.arange(group) % D] = 1.0
+    c.q_dev.copy_(c.q.reshape(-1).to(c.q_dev))
+    out, lse = c.run().result()
+    assert c.status.item() == 0 and kv * ask >= 256 and kv * D >= 256
+    value, key = (x.view(torch.float8_e4m3fn).double().numpy() for x in (of_value, of_key))
+    assert np.array_equal(out.reshape(kv, group, D), np.broadcast_to(value[:, None], (kv, group, D)), equal_nan=True)
+    s = key[:, np.arange(group) % D]
+    tol = bounds(D, 1, 0.0, s, np.zeros((kv, group, 1)), (np.abs(s), np.abs(s)))[1]
+    assert (np.abs(lse.reshape(kv, group) - s) <= tol).all()

@@ -179,7 +179,10 @@ __device__ __forceinline__ const Attend* fresh_args()
 // 131000 tokens 5.0 TB/s in 107 us, a token each of 64 requests, 282 MB, 4.0 TB/s in 70 (a
 // large copy reaches 4.9, read and write).  With more rows, by both HBM and what a tile
 // costs in matrix, vector and LDS instructions, which only partly overlap: 9 rows of 64
-// requests, 292 MB in e4m3, 90 us; 17 rows of 256 requests, 1.9 GB and 242 GFLOP, 516 us.
+// requests, 292 MB in e4m3, 87 us; 17 rows of 256 requests, 1.9 GB and 242 GFLOP, 522 us.
+// Spilled to scratch, read and written once a piece: 19 vector registers of <128, bf16, 3, rows
+// split> (two of them read in the loop over tiles), 8 of <128, e4m3, 3, tokens split>, 18 of
+// <256, e4m3, 1, tokens split>.
 //
 // Sequences are cut into equal shares rather than each into as many pieces: with lengths
 // that differ the longest one no longer decides (the 64 requests' tokens 82 us for 90).
@@ -571,7 +574,9 @@ __global__ __launch_bounds__(kThreads, sv::attend_at_once(DIM, E4M3, TILES, SHAR
                     for (int j = 0; j < 8; ++j) w[j] = exp2_of(w[j]);
                     sum[i] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
                     // rounded to bf16, as the matrix cores take them: half a step of 2^-8 each, as the
-                    // outputs' own rounding is
+                    // outputs' own rounding is (both together are 0.0023 from 64 bits, in the root of the mean
+                    // square relative to the outputs', the latter alone 0.0017; 0.0019 if the reference were the
+                    // row's maximum, whose weight of 1 is exact)
                     p[i - from] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])});
                 }
                 // out^T += V^T P^T

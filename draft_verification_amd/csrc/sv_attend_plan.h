@@ -48,11 +48,16 @@ inline AttendPlan attend_plan(long long B, int kv_heads, int dim, bool e4m3, lon
         p.tiles = (int)n;
     }
     p.rows = p.tiles * 16 * (p.shared ? kAttendWaves : 1);
-    // What a piece of a sequence takes beside its tokens is about that of 256 tokens, more where
-    // more tiles of rows meet at its end, less beside a large tile of tokens.  us with 1, 2 and 4
-    // units: of 64 columns in bf16, one tile of rows, 75, 77 and 81; of 128 in e4m3, three tiles,
-    // 104, 99 and 94, and one 74, 72 and 74; of 256 in bf16, one tile, 55, 60 and 67; of 128 in
-    // bf16, nine tiles, 534, 522 and 526
+    // What a piece of a sequence takes beside its tokens is about that of 256 tokens.  In bf16 with
+    // heads of 256 or one tile of rows it is that of 128, and where the sums of three tiles meet at
+    // its end (tokens split, which e4m3 of 128 columns alone has) that of 512.  us with 1, 2 and 4
+    // units, 64 sequences of 200 to 8000 tokens, eight key-value heads.  Tokens split: bf16, one
+    // tile, of 64 columns 64, 64 and 67, of 128 112, 119 and 121, of 256 219, 217 and 241, two of
+    // 128 122, 122 and 129; e4m3, of 64 one tile 40, 38 and 40, two 49, 45 and 46, of 128 one 67,
+    // 65 and 67, two 81, 79 and 79, three 101, 96 and 90, of 256 one 138, 133 and 138.  Rows split,
+    // nine tiles: bf16, of 64 124, 125 and 130, of 128 202, 202 and 207, of 256 604, 620 and 650;
+    // e4m3, 121, 119 and 126, 178, 174 and 187, and 570, 584 and 612 (here 2 is not the best).
+    // 256 sequences of 500 to 4000, bf16 of 128, nine tiles: 534, 522 and 526
     p.begin = !e4m3 && (dim > 128 || (!p.shared && p.tiles == 1)) ? 1 : !p.shared && p.tiles == 3 ? 4 : 2;
     // As many workgroups as the chip holds at once.  Half as many, and twice: 72 and 64 us for 60,
     // 92 and 72 for 76, 125 and 105 for 99, 817 and 549 for 519

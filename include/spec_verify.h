@@ -594,7 +594,8 @@ typedef struct {
  *                     rows behind its length need and it does not hold yet: the
  *                     lowest free pages, in the order of b.  granted[b] = 1, or 0
  *                     where the sequences up to b need more than there are free
- *                     pages (this one then gets none, SV_STATUS_NO_PAGES).
+ *                     pages (this one then gets none, SV_STATUS_NO_PAGES; one that
+ *                     needs none is granted all the same).
  *   SV_PAGES_COMMIT   lengths[slot] grows by `rows` (or last_row[b] + 1), and the
  *                     pages behind it are given back.
  *   SV_PAGES_RELEASE  the slot's length is 0 and all its pages are given back.
@@ -667,7 +668,9 @@ int spec_verify_pages_copy(spec_verify_t* h, const spec_verify_pages_copy_args* 
 /*
  * Keys and values of one layer: element (page, head, place, d) at keys (values) +
  * page * page_stride + head * head_stride + place * token_stride + d, so that a
- * page may hold its tokens head by head or token by token.
+ * page may hold its tokens head by head or token by token.  Both have the same width,
+ * up to SV_MAX_HEAD_DIM: a cache of one latent row for all heads, wider than that and
+ * with values that are a part of its keys, is not served.
  *   SV_KV_BF16  held in bf16.
  *   SV_KV_E4M3  held in 8 bits: a code stands for its value (e4m3: 1 sign, 4
  *               exponent, 3 fraction bits, largest 448, no infinities) times the
